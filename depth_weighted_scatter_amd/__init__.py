@@ -21,7 +21,11 @@ __all__ = ["BevPoolError", "BevMap", "F32", "F16", "FP8_E4M3", "MAX_TABLE_BYTES"
            "bevpool_forward", "bevpool_forward_baseline", "forward_args",
            "bevpool_forward_ex", "forward_ex_args", "BF16",
            "bevpool_segment_reduce", "segment_reduce_args",
-           "ORDER_TILE_OUTER", "ORDER_DEPTH_OUTER"]
+           "ORDER_TILE_OUTER", "ORDER_DEPTH_OUTER",
+           "Rope", "PagedCache", "PagedBatch", "ROPE_HALVES", "ROPE_ADJACENT", "MAX_HEAD_DIM",
+           "MAX_ROPE_AXES", "bevpool_qk_norm_rope", "bevpool_qk_norm_rope_backward",
+           "bevpool_qk_norm_rope_backward_workspace_size", "bevpool_kv_append",
+           "bevpool_paged_attention", "bevpool_paged_attention_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libbevpool.so")
@@ -338,3 +342,10 @@ def bevpool_segment_reduce(weights: Optional[torch.Tensor], table: torch.Tensor,
     if rc != OK:
         raise BevPoolError("bevpool_segment_reduce", rc)
     return out
+
+
+from .tokens import (MAX_HEAD_DIM, MAX_ROPE_AXES, ROPE_ADJACENT,  # noqa: E402
+                     ROPE_HALVES, PagedBatch, PagedCache, Rope, bevpool_kv_append,
+                     bevpool_paged_attention, bevpool_paged_attention_workspace_size,
+                     bevpool_qk_norm_rope, bevpool_qk_norm_rope_backward,
+                     bevpool_qk_norm_rope_backward_workspace_size)

@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libbevpool.so")
 
-SOURCES = ["bevpool_api.cpp", "map_kernels.hip", "forward_kernels.hip", "baseline_kernels.hip"]
+SOURCES = ["bevpool_api.cpp", "map_kernels.hip", "forward_kernels.hip", "baseline_kernels.hip",
+           "token_api.cpp", "rope_kernels.hip", "attention_kernels.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep hipcc from forming packed fp32 instructions.

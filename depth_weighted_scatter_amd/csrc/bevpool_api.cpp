@@ -58,7 +58,7 @@ const char *bevpool_status_string(int status)
     }
 }
 
-int bevpool_version(void) { return 10000; }
+int bevpool_version(void) { return 10100; }
 
 size_t bevpool_build_map_workspace_size(int32_t n_img, int32_t D, int32_t H, int32_t W,
                                         int64_t n_cells)

@@ -62,7 +62,7 @@ typedef enum bevpool_dtype {
     BEVPOOL_F32 = 0,
     BEVPOOL_F16 = 1,
     BEVPOOL_FP8_E4M3 = 2,
-    BEVPOOL_BF16 = 3   /* output type of bevpool_forward_ex only */
+    BEVPOOL_BF16 = 3   /* output type of bevpool_forward_ex; token operators */
 } bevpool_dtype;
 
 /* Largest feature table (or segment-reduce table) in bytes, 2^32 - 4096.
@@ -300,6 +300,194 @@ int bevpool_forward_baseline(int32_t order, const void *depth, int32_t depth_dty
                              const int32_t *interval_lengths, int32_t n_points,
                              int32_t n_intervals, float *out, int64_t n_cells,
                              hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Token operators.  Once features are pooled, a BEV cell (or a camera pixel, or
+ * a word) is a token with a position -- a point such as (frame, row, column) or
+ * a single index.  The calls below give its queries and keys their norm and
+ * position, keep keys and values of earlier frames in a cache of pages, and
+ * let new tokens read that cache: the gather-reduce of bevpool_segment_reduce
+ * with rows named by a page table and weights that are a softmax of scores.
+ *
+ * Conventions of these calls, beside those above:
+ *   - Head rows have head_dim elements, a multiple of 16 up to
+ *     BEVPOOL_MAX_HEAD_DIM.  Token tensors are [n_tokens, heads, head_dim]
+ *     with the heads of a token contiguous and a stride between tokens (in
+ *     elements, a multiple of 16 bytes, at least heads * head_dim), so
+ *     queries, keys and values may be slices of one packed projection.
+ *     Tensors are 16-byte aligned.
+ *   - Arithmetic is fp32 (angles: fp64); every result is rounded once, to
+ *     nearest-even, to its output type.
+ *   - A call with zero tokens does nothing and returns BEVPOOL_OK (the
+ *     backward still writes zero weight gradients).
+ *   - Asynchronous on `stream`, no allocation, capturable in a HIP graph.
+ */
+#define BEVPOOL_MAX_HEAD_DIM 256
+#define BEVPOOL_MAX_ROPE_AXES 4
+
+/* Which two coordinates of a head row make the rotated pair i (of R/2). */
+typedef enum bevpool_rope_layout {
+    BEVPOOL_ROPE_HALVES = 0,    /* (i, i + R/2) */
+    BEVPOOL_ROPE_ADJACENT = 1   /* (2i, 2i + 1) */
+} bevpool_rope_layout;
+
+/*
+ * bevpool_qk_norm_rope -- RMS norm of every query and key head, then its
+ * rotation by the token's position on several axes, in one pass:
+ *
+ *     n = w * x / sqrt(mean(x^2) + eps)          (n = x without a weight)
+ *     theta_i = positions[axis(i)][token] * inv_freq[i],     i in [0, R/2)
+ *     (n_a, n_b) of pair i  ->  (n_a cos - n_b sin, n_b cos + n_a sin)
+ *
+ * and the coordinates from R on are passed through.  The first
+ * h_sections[0] pairs turn with axis 0, the next h_sections[1] with axis 1,
+ * and so on; R = 2 * sum(h_sections) is a multiple of 16 up to head_dim.
+ * The angle is taken in fp64, so far positions keep theirs.
+ *
+ *   q, k: the input heads, dtype F32, F16 or BF16.  k may be NULL (n_k_heads
+ *       then 0).  q_weight, k_weight [head_dim]: NULL = that one is not
+ *       normed; weight_dtype is dtype or F32 (ignored when both are NULL).
+ *   eps: at least 0 and finite.
+ *   positions [n_axes, n_tokens] int32, inv_freq [R/2] fp32; h_sections
+ *       [n_axes] on the host, n_axes up to BEVPOOL_MAX_ROPE_AXES, 0 = no
+ *       rotation (the three are then ignored).
+ *   q_out, k_out: dtype; each may be its input (same pointer and stride),
+ *       otherwise they do not overlap any input.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, weight_dtype, head_dim, R),
+ * OVERFLOW (n_tokens * (n_q_heads + 2 n_k_heads) beyond 2^31 - 1, n_tokens *
+ * head_dim beyond 2^34, a stride beyond 2^31), HIP.
+ */
+int bevpool_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+                         int32_t head_dim, const void *q_weight, const void *k_weight,
+                         int32_t weight_dtype, float eps, const int32_t *positions,
+                         int32_t n_axes, const int32_t *h_sections, const float *inv_freq,
+                         int32_t layout, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, hipStream_t stream);
+
+/* Bytes of device workspace bevpool_qk_norm_rope_backward needs (0 for
+ * invalid sizes). */
+size_t bevpool_qk_norm_rope_backward_workspace_size(int64_t n_tokens, int32_t n_q_heads,
+                                                    int32_t n_k_heads, int32_t head_dim);
+
+/*
+ * bevpool_qk_norm_rope_backward -- gradients of bevpool_qk_norm_rope.  With g
+ * the output's gradient turned back by -theta and r = 1 / sqrt(mean(x^2) + eps):
+ *
+ *     dx = r * (w g - x r^2 mean(x w g)),     dw = sum over tokens and heads of g x r
+ *
+ * (dx = g without a weight).  The sums of dw are fp32 in a fixed order: the
+ * same call gives the same bits.
+ *
+ *   dq_out, dk_out: gradients of q_out and k_out; q, k: the forward's inputs
+ *       (not read for a side without a weight, and may then be NULL).
+ *   dq, dk: gradients of q and k (dtype); each may be dq_out / dk_out itself
+ *       (same pointer and stride).
+ *   dq_weight, dk_weight [head_dim] fp32, overwritten; required with their
+ *       weight, ignored without.
+ *   workspace: at least bevpool_qk_norm_rope_backward_workspace_size() bytes,
+ *       256-byte aligned; contents on entry are ignored.
+ * Everything else as bevpool_qk_norm_rope.  Errors: also WORKSPACE.
+ */
+int bevpool_qk_norm_rope_backward(const void *dq_out, int64_t dq_out_stride, const void *dk_out,
+                                  int64_t dk_out_stride, const void *q, int64_t q_stride,
+                                  const void *k, int64_t k_stride, int32_t dtype,
+                                  int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,
+                                  int32_t head_dim, const void *q_weight, const void *k_weight,
+                                  int32_t weight_dtype, float eps, const int32_t *positions,
+                                  int32_t n_axes, const int32_t *h_sections,
+                                  const float *inv_freq, int32_t layout, void *dq,
+                                  int64_t dq_stride, void *dk, int64_t dk_stride,
+                                  float *dq_weight, float *dk_weight, void *workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The paged cache, shared by the two calls that follow.
+ *   k_cache, v_cache [n_pages, n_k_heads, page_size, head_dim] of cache_dtype:
+ *       F16, BF16 (the token dtype) or FP8_E4M3 (codes; a stored value is
+ *       code * k_scale or code * v_scale, both between 2^-64 and 2^64; the
+ *       scales are ignored for the other types).  page_size is a power of two
+ *       from 16 to 256.
+ *   q_offsets [n_seqs + 1] int32, non-decreasing: tokens q_offsets[s] to
+ *       q_offsets[s+1] - 1 are the new tokens of sequence s.  Tokens outside
+ *       every sequence are neither read nor written.
+ *   kv_lengths [n_seqs] int32: tokens of sequence s in the cache once its new
+ *       ones are in; its new token i has place
+ *       kv_lengths[s] - (q_offsets[s+1] - q_offsets[s]) + i.
+ *   block_table [n_seqs, max_pages] int32: place p of sequence s is slot
+ *       p % page_size of page block_table[s][p / page_size].  An entry outside
+ *       [0, n_pages) is no page: its places hold no key (a cache may drop
+ *       pages that left the window, and mark them -1).
+ * n_seqs is at most 2^24; n_seqs * max_pages, max_pages * page_size and
+ * n_pages * page_size stay below 2^31 (else OVERFLOW).
+ * Offsets are clipped to [0, n_tokens] and lengths to
+ * [0, max_pages * page_size], so no value of these arrays makes a call read
+ * or write outside its tensors.
+ */
+
+/*
+ * bevpool_kv_append -- put the new tokens' keys and values into their pages,
+ * the keys normed and rotated on the way as bevpool_qk_norm_rope does; the
+ * queries, if given, get the same in the same launch.
+ *
+ *   k, v (dtype F16 or BF16): new keys and values; q, q_out: queries (NULL =
+ *       none, n_q_heads then 0).  q_out may be q.
+ *   cache_dtype FP8_E4M3: the value divided by its scale, clamped to +-448
+ *       and rounded to nearest-even (NaN stays NaN).
+ * Queries of tokens inside a sequence are always written; keys and values of
+ * a token whose place is negative, past the table or on no page are dropped.
+ * Two tokens of one call must not share a slot.  Errors: INVALID_ARG,
+ * UNSUPPORTED, OVERFLOW, HIP.
+ */
+int bevpool_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, int32_t dtype, int64_t n_tokens,
+                      int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+                      const void *q_weight, const void *k_weight, int32_t weight_dtype,
+                      float eps, const int32_t *positions, int32_t n_axes,
+                      const int32_t *h_sections, const float *inv_freq, int32_t layout,
+                      void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                      int32_t cache_dtype, float k_scale, float v_scale, int64_t n_pages,
+                      int32_t page_size, const int32_t *q_offsets, const int32_t *kv_lengths,
+                      int32_t n_seqs, const int32_t *block_table, int32_t max_pages,
+                      hipStream_t stream);
+
+/*
+ * Bytes of device workspace bevpool_paged_attention needs for these sizes (0
+ * for invalid ones; never 0 for valid ones).
+ */
+size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
+                                              int32_t n_q_heads, int32_t n_k_heads,
+                                              int32_t head_dim, int32_t page_size,
+                                              int32_t max_pages);
+
+/*
+ * bevpool_paged_attention -- attention of the new tokens over their
+ * sequence's cached keys and values (the new tokens' own among them):
+ *
+ *     out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / (n_q_heads / n_k_heads)]) v[j, ..]
+ *
+ * over the places j in [0, kv_lengths[s]) that are on a page and, with p the
+ * place of token t, satisfy j <= p if causal and j > p - window if window > 0.
+ * A token that sees no key gets 0.  Keys and values in hidden places have no
+ * influence, infinities and NaN among them.  Chunks, single tokens, or both
+ * in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
+ * statistics and sums are fp32; the weights enter the product with v rounded
+ * to the token dtype (F16 for an FP8_E4M3 cache).
+ *
+ *   q, out: dtype F16 or BF16; scale positive and finite; window 0 = none.
+ *   workspace: at least bevpool_paged_attention_workspace_size() bytes,
+ *       256-byte aligned, contents on entry ignored; calls that may overlap
+ *       in time need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, WORKSPACE, HIP.
+ */
+int bevpool_paged_attention(const void *q, int64_t q_stride, int32_t dtype, int64_t n_tokens,
+                            int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+                            const void *k_cache, const void *v_cache, int32_t cache_dtype,
+                            float k_scale, float v_scale, int64_t n_pages, int32_t page_size,
+                            const int32_t *q_offsets, const int32_t *kv_lengths, int32_t n_seqs,
+                            const int32_t *block_table, int32_t max_pages, float scale,
+                            int32_t causal, int32_t window, void *out, int64_t out_stride,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

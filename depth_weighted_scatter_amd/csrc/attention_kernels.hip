@@ -1,4 +1,24 @@
 // Attention over a paged cache (gfx950).  See bevpool.h for the definition.
+//
+// The query heads that share a key head are rows of one product: the rows of
+// a (sequence, key head) are r = token * G + g, G = n_q_heads / n_k_heads.  A
+// block takes up to 128 consecutive rows and a range of keys, in one of two
+// ways: with more than 32 rows each of its four waves owns 32 rows and all
+// walk the keys together ("rows"); with 32 or fewer every wave takes the same
+// rows and every fourth tile of 32 keys ("keys"), and the waves join at the
+// end.  Ranges of keys are cut over blocks when rows alone do not fill the
+// chip, and attend_join adds their parts.
+//
+// Both products run on 32 x 32 x 16 matrix instructions, transposed:
+//     S^T [keys x rows] = K Q^T,      O^T [dim x rows] += V^T P^T,
+// so a row of the softmax is a column of the result: a lane holds 16 of its
+// column's 32 keys, its maximum and sum need one exchange between the two
+// halves of the wave, and rescaling O is a multiplication by a lane's own
+// scalar.  The result registers of S^T hold keys 8 (i / 4) + 4 half + i % 4;
+// taken as the second product's inner index in that order they are its
+// operand as they stand, and V^T is read from LDS in the same order by the
+// transposing read (four keys of one dim a lane), so the weights never leave
+// their registers.
 #include <hip/hip_runtime.h>
 
 #include "token_device.h"
@@ -8,102 +28,829 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kWavesPerBlock = kBlock / kLanes;
+constexpr int kRowsPerWave = 32;
+constexpr int kRowsPerBlock = kWavesPerBlock * kRowsPerWave;
+constexpr int kUnit = 128;            // keys: ranges of a split are multiples of this
+constexpr int kMinUnits = 4;          // and at least this many
 constexpr float kLog2e = 1.44269504088896340736f;
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
+
+// Type in which keys meet queries, and values meet weights.  e4m3 widens
+// exactly to either 16-bit type; fp16 rounds the weights 8 times finer.
+template <int DT, int CDT> struct Types { static constexpr int V = CDT == kE4M3 ? int(kF16) : DT; };
+
+template <int DT> struct Frag;
+template <> struct Frag<kF16> { using type = f16x8; };
+template <> struct Frag<kBF16> { using type = bf16x8; };
+
 template <int DT>
-__device__ __forceinline__ float element(const void *base, int64_t i)
+__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c)
 {
-    if constexpr (DT == kE4M3) {
-        const int w = static_cast<const uint8_t *>(base)[i];
-        return __builtin_amdgcn_cvt_f32_fp8(w, 0);
+    using F = typename Frag<DT>::type;
+    if constexpr (DT == kF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(F, a),
+                                                      __builtin_bit_cast(F, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(F, a),
+                                                       __builtin_bit_cast(F, b), c, 0, 0, 0);
+}
+
+// LDS tiles: key and value rows one after the other, in 16-byte pieces, with
+// the pieces of a row permuted (a direct load to LDS writes consecutive
+// addresses, so rows cannot be padded).  Keys: a phase of a 16-byte read
+// takes one piece of 16 consecutive keys; the permutation sends those to 16
+// different bank groups.  Values: a phase of a transposing read takes 64
+// bytes of four consecutive keys; they go to four different quarters of the
+// 256 bytes of banks (a row of 10 pieces shares a few).
+template <int DP> struct Tiles {
+    static constexpr int kSteps = DP / 16;                 // inner steps of K Q^T
+    static constexpr int kDims = (DP + 31) / 32;           // 32-row pieces of O^T
+    static constexpr int kPieces = DP / 8;                 // 16-byte pieces of a row
+    static constexpr int kRow = DP * 2;
+    static constexpr int kRound = kPieces & -kPieces;      // largest power of 2 in kPieces
+    static constexpr int kSpread = kRound < 16 ? kRound : 16;
+    static constexpr int kBuffers = 8 * 32 * kRow;         // keys and values of 128 keys
+    static constexpr int kSumRow = DP + 4;                 // floats of a row on the way out
+    static constexpr int kSums = kWavesPerBlock * 32 * kSumRow * 4;
+    // room past the last row: the last 32-dim piece of a 16-dim remainder reads it
+    static constexpr int kLds = (kBuffers > kSums ? kBuffers : kSums) + 64;
+
+    static __device__ __forceinline__ int key_swizzle(int key)
+    {
+        return (key / (16 / kSpread)) & (kSpread - 1);
+    }
+    static __device__ __forceinline__ int value_swizzle(int key)
+    {
+        if constexpr (kPieces % 16 == 0) return (key & 3) << 2;
+        else if constexpr (kPieces % 8 == 0) return ((key >> 1) & 1) << 2;
+        else return 0;
+    }
+};
+
+// What a block (or a row of attend_join) works on.
+struct Plan {
+    int seq, begin, q_len;     // sequence, its first token, its new tokens
+    int len;                   // its cached tokens
+    int row0, rows;            // first row of the tile, rows in it
+    int lo, hi;                // keys any of them sees: [lo, hi), lo a multiple of 64
+    int per;                   // keys of one split
+    int splits;                // splits that have keys (at least 1)
+};
+
+__device__ __forceinline__ void row_limits(const AttnParams &p, const Plan &w, int row, int group,
+                                           int &lo, int &hi)
+{
+    const int64_t place = int64_t(w.len) - w.q_len + row / group;
+    int64_t h = p.causal ? place + 1 : w.len, l = p.window > 0 ? place - p.window + 1 : 0;
+    h = h < 0 ? 0 : (h > w.len ? w.len : h);
+    l = l < 0 ? 0 : (l > w.len ? w.len : l);
+    lo = int(l);
+    hi = int(h);
+}
+
+// Fills in everything of w that follows from seq, begin, q_len, len, row0.
+__device__ __forceinline__ void plan_keys(const AttnParams &p, Plan &w, int group, int max_splits)
+{
+    const int left = w.q_len * group - w.row0;
+    w.rows = left < kRowsPerBlock ? left : kRowsPerBlock;
+    int lo, hi, unused;
+    row_limits(p, w, w.row0, group, lo, unused);
+    row_limits(p, w, w.row0 + w.rows - 1, group, unused, hi);
+    w.lo = lo & ~63;
+    w.hi = hi > w.lo ? hi : w.lo;
+    const int units = (w.hi - w.lo + kUnit - 1) / kUnit;
+    int per = (units + max_splits - 1) / max_splits;
+    per = per < kMinUnits ? kMinUnits : per;
+    w.per = per * kUnit;
+    w.splits = units > per ? (units + per - 1) / per : 1;
+}
+
+__device__ __forceinline__ void plan_sequence(const AttnParams &p, Plan &w, int seq, int begin, int end)
+{
+    const PagedParams &g = p.paged;
+    const int64_t room = int64_t(g.max_pages) << g.page_shift;
+    const int len = g.kv_lengths[seq];
+    w.seq = seq;
+    w.begin = begin;
+    w.q_len = end - begin;
+    w.len = len < 0 ? 0 : (len < room ? len : int(room));
+}
+
+// One wave's rows: their part of O^T, running maximum of the scores (before
+// the scale) and this lane's part of the weights' sum.
+template <int DP> struct Rows {
+    f32x16 o[Tiles<DP>::kDims];
+    float top, sum;
+};
+
+// 16-bit values with all exponent bits set (infinity, NaN) in a dword pair.
+template <int VT>
+__device__ __forceinline__ bool non_finite(u32x4 v)
+{
+    constexpr uint32_t m = VT == kF16 ? 0x7c00u : 0x7f80u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad |= (v[i] & m) == m || ((v[i] >> 16) & m) == m;
+    return bad;
+}
+
+template <int VT>
+__device__ __forceinline__ u32x4 finite_only(u32x4 v)
+{
+    constexpr uint32_t m = VT == kF16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t x = v[i];
+        if ((x & m) == m) x &= 0xffff0000u;
+        if (((x >> 16) & m) == m) x &= 0xffffu;
+        v[i] = x;
+    }
+    return v;
+}
+
+// Eight e4m3 codes as DT (exact).
+template <int DT>
+__device__ __forceinline__ u32x4 widen(u32x2 raw)
+{
+    if constexpr (DT == kF16) {
+        const int a = int(raw.x), b = int(raw.y);
+        u32x4 w;
+        w.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false));
+        w.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true));
+        w.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
+        w.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
+        return w;
     } else {
-        return float(static_cast<const typename Elem<DT>::type *>(base)[i]);
+        const int a = int(raw.x), b = int(raw.y);
+        u32x4 w;
+        w.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false));
+        w.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true));
+        w.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false));
+        w.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true));
+        return w;
     }
 }
 
-// One wave for each (token, query head): keys one after the other, the lanes
-// over the head's elements, running maximum and sum of the softmax.
-template <int DT, int CDT>
-__global__ __launch_bounds__(kBlock) void attend_rows(AttnParams p)
+__device__ const u32x4 kZeroPiece = {0, 0, 0, 0};
+
+// One 16-byte piece for each lane, straight from memory to LDS: lane i's goes
+// to lds + 16 i.  Not seen by the compiler's wait counts: a wait_loads<n>
+// before the data is used is the caller's.
+__device__ __forceinline__ void load_to_lds(const void *from, const char *lds)
+{
+    const uint32_t at = __builtin_amdgcn_readfirstlane(
+        uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)lds)));
+    // an M0 write and the load that uses it need a wait state between them
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(from), "s"(at)
+                 : "memory");
+}
+
+// Waits until at most N of the wave's memory reads are pending (they complete
+// in order).
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+// Brings tiles of KEYS keys to LDS.  The keys of a tile are 16-key groups, each
+// on one page; lane i of a wave keeps the page of the i-th group to come, 64
+// groups at a time.  Groups on no page, or past `end`, are read from page 0
+// and hidden later, so every read is inside the cache.
+//
+// WAVES waves share a tile; 16-bit caches go straight to LDS, e4m3 ones are
+// read into registers (fetch) and widened on the way to LDS (store).
+template <int DT, int CDT, int DP, int KEYS, int WAVES>
+struct Stage {
+    using L = Tiles<DP>;
+    static constexpr int VT = Types<DT, CDT>::V;
+    static constexpr bool kDirect = CDT != kE4M3;
+    static constexpr int kGroups = KEYS / 16;
+    static constexpr int kLoads = KEYS * L::kPieces / kLanes;       // 64-lane loads of a tile
+    static constexpr int kSlots = (kLoads + WAVES - 1) / WAVES;     // of them, a wave's
+    static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of pages
+    using C = typename Elem<CDT>::type;
+
+    const AttnParams &p;
+    const int32_t *table;
+    int kv_head, wave, end, first, stride;     // tile t holds keys first + t * stride ...
+    int pages;                                 // lane's group's page, -1 for none
+    u32x2 k[kDirect ? 1 : kSlots], v[kDirect ? 1 : kSlots];
+
+    __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
+                     int stride, int end)
+        : p(p), table(p.paged.block_table + int64_t(w.seq) * p.paged.max_pages), kv_head(kv_head),
+          wave(wave), end(end), first(first), stride(stride)
+    {
+    }
+
+    __device__ __forceinline__ void find_pages(int tile)
+    {
+        const int lane = int(threadIdx.x) & (kLanes - 1);
+        const int64_t key = first + int64_t(tile + lane / kGroups) * stride + lane % kGroups * 16;
+        pages = -1;
+        if (key < end) pages = table[key >> p.paged.page_shift];
+        if (pages >= p.paged.n_pages) pages = -1;
+    }
+
+    // One bit for each 16-key group of the tile that is on a page.
+    __device__ __forceinline__ uint32_t groups_there(int tile) const
+    {
+        return uint32_t(__ballot(pages >= 0) >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
+    }
+
+    // First element of the tile's group in the cache.
+    __device__ __forceinline__ int64_t group_at(int tile, int group) const
+    {
+        const PagedParams &g = p.paged;
+        const int page = max(__builtin_amdgcn_readlane(pages, tile % kBatch * kGroups + group), 0);
+        const int key = first + tile * stride + group * 16;
+        return (((int64_t(page) * p.n_k_heads + kv_head) << g.page_shift) +
+                (key & ((1 << g.page_shift) - 1))) * p.head_dim;
+    }
+
+    // This lane's piece of load m: its address in the cache and its key.
+    template <bool VALUES>
+    __device__ __forceinline__ const C *source(const int64_t (&at)[kGroups], int m, int &key) const
+    {
+        const int id = m * kLanes + (int(threadIdx.x) & (kLanes - 1));
+        key = id / L::kPieces;
+        const int piece = (id % L::kPieces) ^ (VALUES ? L::value_swizzle(key) : L::key_swizzle(key));
+        int64_t base;
+        if constexpr (L::kPieces % 4 == 0) {          // a load stays within one group
+            base = at[m / (L::kPieces / 4)];
+        } else {
+            base = at[0];
+#pragma unroll
+            for (int i = 1; i < kGroups; ++i) base = key / 16 == i ? at[i] : base;
+        }
+        const C *cache = static_cast<const C *>(VALUES ? p.paged.v_cache : p.paged.k_cache);
+        const C *from = cache + base + (key % 16) * p.head_dim + piece * 8;
+        if (DP != p.head_dim && piece * 8 >= p.head_dim)
+            from = reinterpret_cast<const C *>(&kZeroPiece);
+        return from;
+    }
+
+    // Issues a tile's reads of keys or of values.
+    template <bool VALUES>
+    __device__ __forceinline__ void fetch(int tile, const char *lds)
+    {
+        int64_t at[kGroups];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) at[i] = group_at(tile, i);
+#pragma unroll
+        for (int n = 0; n < kSlots; ++n) {
+            const int m = n * WAVES + wave;
+            if (kLoads % WAVES != 0 && m >= kLoads) continue;
+            int key;
+            const C *from = source<VALUES>(at, m, key);
+            if constexpr (kDirect) load_to_lds(from, lds + m * 1024);
+            else (VALUES ? v : k)[n] = *reinterpret_cast<const u32x2 *>(from);
+        }
+    }
+
+    // e4m3: what fetch read, widened, to LDS.
+    template <bool VALUES>
+    __device__ __forceinline__ void store(char *lds)
+    {
+        if constexpr (!kDirect) {
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n) {
+                const int m = n * WAVES + wave;
+                if (kLoads % WAVES != 0 && m >= kLoads) continue;
+                const u32x2 x = (VALUES ? v : k)[n];
+                *reinterpret_cast<u32x4 *>(lds + m * 1024 + (int(threadIdx.x) & (kLanes - 1)) * 16) =
+                    widen<VALUES ? VT : DT>(x);
+            }
+        }
+    }
+
+    // Values of places that no row sees become zeros (the tail of a page may
+    // hold anything, and 0 * NaN is not 0); so do infinities and NaN that some
+    // rows see and others do not, which set bad.
+    __device__ __forceinline__ void clean_values(char *lds, int tile, uint32_t there, int *bad)
+    {
+        const int key0 = first + tile * stride;
+#pragma unroll 1
+        for (int n = 0; n < kSlots; ++n) {
+            const int m = n * WAVES + wave;
+            if (m >= kLoads) continue;
+            const int id = m * kLanes + (int(threadIdx.x) & (kLanes - 1));
+            const int key = id / L::kPieces;
+            u32x4 *at = reinterpret_cast<u32x4 *>(lds + id * 16);
+            if (key0 + key >= end || !((there >> (key / 16)) & 1)) {
+                *at = 0;
+            } else if (non_finite<VT>(*at)) {
+                *at = finite_only<VT>(*at);
+                *bad = 1;
+            }
+        }
+    }
+};
+
+// S^T of one tile for a wave's rows.
+template <int DT, int DP, int KT>
+__device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<DP>::kSteps],
+                                       const char *keys)
+{
+    using L = Tiles<DP>;
+    const int lane = int(threadIdx.x) & (kLanes - 1);
+    const int col = lane & 31, piece = (lane >> 5) ^ L::key_swizzle(col);
+    const char *row = keys + col * L::kRow;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+        s[kt] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < L::kSteps; ++st)
+            s[kt] = mfma<DT>(*reinterpret_cast<const u32x4 *>(row + kt * 32 * L::kRow +
+                                                              ((piece ^ (2 * st)) << 4)),
+                             q[st], s[kt]);
+    }
+}
+
+// Hides what a row does not see: key j of the tile is seen in [lo, hi)
+// (relative to the tile) if its 16-key group is there.
+template <int KT>
+__device__ __forceinline__ void hide(f32x16 (&s)[KT], int lo, int hi, uint32_t there)
+{
+    const int half = (int(threadIdx.x) & (kLanes - 1)) >> 5;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int key = kt * 32 + 8 * (i / 4) + 4 * half + i % 4;
+            const bool seen = key >= lo && key < hi && ((there >> (kt * 2 + i / 8)) & 1);
+            s[kt][i] = seen ? s[kt][i] : -INFINITY;
+        }
+}
+
+// Scores to weights: the running maximum and sum, O rescaled where the
+// maximum moved, the weights in w as operands of the second product.
+template <int VT, int DP, int KT>
+__device__ __forceinline__ void weights(Rows<DP> &r, f32x16 (&s)[KT], u32x4 (&w)[2 * KT], float c)
+{
+    float top = s[0][0];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // The reference maximum moves only when a row's weights would pass 2^8:
+    // any reference within that of the true maximum gives the same softmax,
+    // and most tiles then leave O as it is.
+    if (__any(top * c > r.top * c + 8.0f || (r.top == -INFINITY && top > -INFINITY))) {
+        const float now = fmaxf(r.top, top);
+        const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
+        r.top = now;
+        r.sum *= keep;
+#pragma unroll
+        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] *= keep;
+    }
+    const float base = r.top == -INFINITY ? 0.0f : r.top * c;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[kt][i] = __builtin_amdgcn_exp2f(fmaf(s[kt][i], c, -base));
+            r.sum += s[kt][i];
+        }
+        const f32x8 a = __builtin_shufflevector(s[kt], s[kt], 0, 1, 2, 3, 4, 5, 6, 7);
+        const f32x8 b = __builtin_shufflevector(s[kt], s[kt], 8, 9, 10, 11, 12, 13, 14, 15);
+        using F = typename Frag<VT>::type;
+        w[2 * kt] = __builtin_bit_cast(u32x4, __builtin_convertvector(a, F));
+        w[2 * kt + 1] = __builtin_bit_cast(u32x4, __builtin_convertvector(b, F));
+    }
+}
+
+// O^T += V^T P^T.
+template <int VT, int DP, int KT>
+__device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT], const char *values)
+{
+    using L = Tiles<DP>;
+    using Lds = __attribute__((address_space(3))) i16x4;
+    const int lane = int(threadIdx.x) & (kLanes - 1);
+    // lane i of 16 names key i / 4, four dims from 4 (i % 4), and gets dim i, keys 0-3
+    const int key = 4 * (lane >> 5) + (lane & 15) / 4;
+    const int in_row = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    const int swizzle = L::value_swizzle(key) >> 2;
+    const char *from = values + key * L::kRow + in_row;
+#pragma unroll
+    for (int u = 0; u < KT * 2; ++u)
+#pragma unroll
+        for (int dt = 0; dt < L::kDims; ++dt) {
+            const char *at = from + u * 16 * L::kRow + ((dt ^ swizzle) << 6);
+            const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)at);
+            const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at + 8 * L::kRow));
+            const u32x2 xx = __builtin_bit_cast(u32x2, x), yy = __builtin_bit_cast(u32x2, y);
+            r.o[dt] = mfma<VT>(u32x4{xx.x, xx.y, yy.x, yy.y}, w[u], r.o[dt]);
+        }
+}
+
+// The infinities and NaN of four dims among the values that a row sees, added
+// up (0 if there are none): any weight times one of them is it.  Keys in
+// [lo, hi) that are on a page.
+template <int CDT>
+__device__ f32x4 non_finite_sum(const AttnParams &p, const int32_t *table, int kv_head, int d,
+                                int lo, int hi)
+{
+    using C = typename Elem<CDT>::type;
+    const PagedParams &g = p.paged;
+    f32x4 sum = 0.0f;
+    for (int key = lo; key < hi; ++key) {
+        const int at = table[key >> g.page_shift];
+        if (at < 0 || at >= g.n_pages) continue;
+        const int64_t row = ((int64_t(at) * p.n_k_heads + kv_head) << g.page_shift) +
+                            (key & ((1 << g.page_shift) - 1));
+        const C *e = static_cast<const C *>(g.v_cache) + row * p.head_dim + d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x;
+            if constexpr (CDT == kE4M3) x = __builtin_amdgcn_cvt_f32_fp8(int(e[i]), 0);
+            else x = float(e[i]);
+            if (!__builtin_isfinite(x)) sum[i] += x;
+        }
+    }
+    return sum;
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(typename Elem<DT>::type *p, f32x4 v)
+{
+    typedef typename Elem<DT>::type T4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<T4 *>(p) = __builtin_convertvector(v, T4);
+}
+
+struct Parts {
+    float2 *stats;        // [splits][rows]: maximum * c, sum of weights
+    float *o;             // [splits][rows][head_dim]
+    int64_t rows;         // n_tokens * n_q_heads
+};
+
+template <int DT, int CDT, int DP>
+__global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p, Parts parts,
+                                                                   int tiles, int max_splits)
 {
     using T = typename Elem<DT>::type;
-    constexpr int kPer = kMaxHeadDim / kLanes;
+    using L = Tiles<DP>;
+    constexpr int VT = Types<DT, CDT>::V;
+    __shared__ __attribute__((aligned(16))) char lds[L::kLds];
+    __shared__ int bad;          // a hidden place may hold a value that is not finite
+    __shared__ float wave_stats[kWavesPerBlock][32][2];
+
+    const PagedParams &g = p.paged;
+    const int lane = int(threadIdx.x) & (kLanes - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kLanes);
+    const int col = lane & 31, half = lane >> 5;
+    const int group = p.n_q_heads / p.n_k_heads;
+    // heads vary fastest: blocks go to the XCDs in turn, so that with eight
+    // key heads each XCD's L2 serves one; long tiles (late rows) start first
+    const int kv_head = int(blockIdx.x) % p.n_k_heads;
+    const int tile = tiles - 1 - int(blockIdx.x) / p.n_k_heads;
+    const int split = int(blockIdx.y);
+
+    // The sequence whose tiles include this one.  Its tiles start at
+    // off * G / 128 + seq: every sequence has room for all of its rows, and
+    // the start grows with it.
+    const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
+    const auto start = [&](int i) { return int64_t(off(i)) * group / kRowsPerBlock + i; };
+    const int seq = count_upto(g.n_seqs, tile, start);
+    if (seq >= g.n_seqs) return;
+    const int begin = off(seq), end = off(seq + 1);
+    const int64_t row0 = (tile - start(seq)) * kRowsPerBlock;
+    if (row0 < 0 || row0 >= int64_t(end - begin) * group) return;
+    Plan w;
+    plan_sequence(p, w, seq, begin, end);
+    w.row0 = int(row0);
+    plan_keys(p, w, group, max_splits);
+    if (split >= w.splits) return;
+    const int from = w.lo + split * w.per;
+    const int to = min(w.hi, from + w.per);
+    const bool by_keys = w.rows <= kRowsPerWave;
+
+    // this lane's row, its limits, and its queries (rows past the last repeat it)
+    const int first = by_keys ? 0 : wave * kRowsPerWave;
+    const int row = w.row0 + min(first + col, w.rows - 1);
+    const int token = begin + row / group, head = kv_head * group + row % group;
+    int lo, hi;
+    row_limits(p, w, row, group, lo, hi);
+    u32x4 q[L::kSteps];
+    {
+        const T *src = static_cast<const T *>(p.q) + int64_t(token) * p.q_stride +
+                       int64_t(head) * p.head_dim + half * 8;
+#pragma unroll
+        for (int st = 0; st < L::kSteps; ++st)
+            q[st] = st * 16 < p.head_dim ? *reinterpret_cast<const u32x4 *>(src + st * 16) : u32x4(0u);
+    }
+    // limits of all of the wave's rows (they grow with the row)
+    const int wave_lo = __shfl(lo, 0), wave_hi = __shfl(hi, 31);
+    const int all_lo = __shfl(lo, 31), all_hi = __shfl(hi, 0);
+    const float c = p.scale * g.k_scale * kLog2e;
+
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    Rows<DP> r;
+    r.top = -INFINITY;
+    r.sum = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < L::kDims; ++dt) r.o[dt] = 0.0f;
+
+    if (!by_keys) {
+        // two buffers of 64 keys: a tile's reads run while the one before it
+        // is worked on
+        using S = Stage<DT, CDT, DP, 64, kWavesPerBlock>;
+        S st(p, w, kv_head, wave, from, 64, to);
+        constexpr int kHalf = 64 * L::kRow;
+        // keys that every row of the block sees; elsewhere values are looked at
+        int blo, bhi, unused;
+        row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
+        row_limits(p, w, w.row0, group, unused, bhi);
+        bhi = min(bhi, to);
+        const int n_tiles = (to - from + 63) / 64;
+        if (n_tiles > 0) {
+            st.find_pages(0);
+            st.template fetch<false>(0, lds);
+            st.template fetch<true>(0, lds + kHalf);
+        }
+        uint32_t there = n_tiles > 0 ? st.groups_there(0) : 0;
+        for (int tile = 0; tile < n_tiles; ++tile) {
+            char *keys = lds + (tile & 1) * 2 * kHalf, *values = keys + kHalf;
+            const int key0 = from + tile * 64;
+            if constexpr (S::kDirect) {
+                wait_loads<0>();
+            } else {
+                st.template store<false>(keys);
+                st.template store<true>(values);
+            }
+            __syncthreads();
+            const uint32_t now = there;
+            if (tile + 1 < n_tiles) {
+                if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
+                there = st.groups_there(tile + 1);
+                char *next = lds + ((tile + 1) & 1) * 2 * kHalf;
+                st.template fetch<false>(tile + 1, next);
+                st.template fetch<true>(tile + 1, next + kHalf);
+            }
+            if (key0 < blo || key0 + 64 > bhi || now != 15) {
+                st.clean_values(values, tile, now, &bad);
+                __syncthreads();
+            }
+            if (key0 < wave_hi && key0 + 64 > wave_lo) {
+                f32x16 s[2];
+                u32x4 x[4];
+                scores<DT, DP, 2>(s, q, keys);
+                if (key0 < all_lo || key0 + 64 > min(all_hi, to) || now != 15)
+                    hide<2>(s, lo - key0, min(hi, to) - key0, now);
+                weights<VT, DP, 2>(r, s, x, c);
+                add_values<VT, DP, 2>(r, x, values);
+            }
+        }
+    } else {
+        // a buffer of 32 keys for each wave: the next keys are read once the
+        // scores are done with these, the next values once O is
+        using S = Stage<DT, CDT, DP, 32, 1>;
+        constexpr int kStep = 32 * kWavesPerBlock;
+        constexpr int kHalf = 32 * L::kRow;
+        const int first_key = from + wave * 32;
+        S st(p, w, kv_head, 0, first_key, kStep, to);
+        char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
+        const int n_tiles = to > first_key ? (to - first_key + kStep - 1) / kStep : 0;
+        if (n_tiles > 0) {
+            st.find_pages(0);
+            st.template fetch<false>(0, keys);
+            st.template fetch<true>(0, values);
+        }
+        for (int tile = 0; tile < n_tiles; ++tile) {
+            const int key0 = first_key + tile * kStep;
+            const bool more = tile + 1 < n_tiles;
+            const uint32_t there = st.groups_there(tile);
+            f32x16 s[1];
+            u32x4 x[2];
+            if constexpr (S::kDirect) {
+                wait_loads<S::kSlots>();                 // the values may be on their way
+            } else {
+                st.template store<false>(keys);
+                st.template store<true>(values);
+            }
+            scores<DT, DP, 1>(s, q, keys);
+            if (more) {
+                if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
+                wait_lds();
+                st.template fetch<false>(tile + 1, keys);
+                if constexpr (!S::kDirect) st.template fetch<true>(tile + 1, values);
+            }
+            const bool whole = key0 >= all_lo && key0 + 32 <= min(all_hi, to) && there == 3;
+            if (!whole) hide<1>(s, lo - key0, min(hi, to) - key0, there);
+            weights<VT, DP, 1>(r, s, x, c);
+            if constexpr (S::kDirect) {
+                if (more) wait_loads<S::kSlots>();
+                else wait_loads<0>();
+            }
+            if (!whole) st.clean_values(values, tile, there, &bad);
+            add_values<VT, DP, 1>(r, x, values);
+            if constexpr (S::kDirect) {
+                wait_lds();
+                if (more) st.template fetch<true>(tile + 1, values);
+            }
+        }
+    }
+    r.sum += __shfl_xor(r.sum, 32);
+
+    // Every wave's O goes through LDS, so that stores are whole rows; the
+    // waves of a tile by keys bring theirs to a common maximum and are added.
+    if (half == 0) {
+        wave_stats[wave][col][0] = r.top;
+        wave_stats[wave][col][1] = r.sum;
+    }
+    __syncthreads();
+    const auto weight = [&](float t, float top) {
+        return t == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((t - top) * c);
+    };
+    constexpr int kRow = L::kSumRow;
+    float *all = reinterpret_cast<float *>(lds);      // [wave][row][kRow]
+    if (first + col < w.rows) {
+        float keep = 1.0f;
+        if (by_keys) {
+            float top = r.top;
+#pragma unroll
+            for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, wave_stats[i][col][0]);
+            keep = weight(r.top, top);
+        }
+#pragma unroll
+        for (int dt = 0; dt < L::kDims; ++dt)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int d = dt * 32 + 8 * b + 4 * half;
+                if (d >= DP) continue;
+                f32x4 x = {r.o[dt][4 * b], r.o[dt][4 * b + 1], r.o[dt][4 * b + 2], r.o[dt][4 * b + 3]};
+                *reinterpret_cast<f32x4 *>(all + (wave * 32 + col) * kRow + d) = x * keep;
+            }
+    }
+    __syncthreads();
+    const int fours = p.head_dim / 4;
+    for (int i = int(threadIdx.x); i < w.rows * fours; i += kBlock) {
+        const int n = i / fours, d = (i - n * fours) * 4;
+        f32x4 x;
+        float top, sum;
+        if (by_keys) {
+            x = 0.0f;
+            top = -INFINITY;
+            sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWavesPerBlock; ++k) {
+                x += *reinterpret_cast<const f32x4 *>(all + (k * 32 + n) * kRow + d);
+                top = fmaxf(top, wave_stats[k][n][0]);
+            }
+#pragma unroll
+            for (int k = 0; k < kWavesPerBlock; ++k)
+                if (wave_stats[k][n][1] != 0.0f)
+                    sum += wave_stats[k][n][1] * weight(wave_stats[k][n][0], top);
+        } else {
+            x = *reinterpret_cast<const f32x4 *>(all + n * kRow + d);
+            top = wave_stats[n / 32][n % 32][0];
+            sum = wave_stats[n / 32][n % 32][1];
+        }
+        const int row = w.row0 + n;
+        const int64_t t = begin + row / group;
+        const int h = kv_head * group + row % group;
+        if (bad) {
+            int lo, hi;
+            row_limits(p, w, row, group, lo, hi);
+            x += non_finite_sum<CDT>(p, g.block_table + int64_t(w.seq) * g.max_pages, kv_head, d,
+                                     max(lo, from), min(hi, to));
+        }
+        if (w.splits == 1) {
+            x *= sum == 0.0f ? 0.0f : g.v_scale / sum;
+            store4<DT>(static_cast<T *>(p.out) + t * p.out_stride + int64_t(h) * p.head_dim + d, x);
+        } else {
+            const int64_t at = split * parts.rows + t * p.n_q_heads + h;
+            *reinterpret_cast<f32x4 *>(parts.o + at * p.head_dim + d) = x;
+            if (d == 0) parts.stats[at] = make_float2(top * c, sum);
+        }
+    }
+}
+
+// Adds the splits of a row: one wave for each (token, query head), a lane for
+// four dims.  Rows of one split are already in place.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void attend_join(AttnParams p, Parts parts, int max_splits)
+{
+    using T = typename Elem<DT>::type;
     const PagedParams &g = p.paged;
     const int lane = int(threadIdx.x) & (kLanes - 1);
     const int64_t row = int64_t(blockIdx.x) * kWavesPerBlock + int(threadIdx.x) / kLanes;
-    if (row >= int64_t(p.n_tokens) * p.n_q_heads) return;
+    if (row >= parts.rows) return;
     const int token = int(row / p.n_q_heads), head = int(row % p.n_q_heads);
-    const int kv_head = head / (p.n_q_heads / p.n_k_heads);
-    const auto off = [&](int i) { return int64_t(clip(g.q_offsets[i], 0, p.n_tokens)); };
-    const int seq = count_upto(g.n_seqs, token, off);
-    if (seq >= g.n_seqs || token < off(seq) || token >= off(seq + 1)) return;
-    const int begin = int(off(seq)), end = int(off(seq + 1));
-    const int64_t room = int64_t(g.max_pages) << g.page_shift;
-    const int64_t len = g.kv_lengths[seq] < 0 ? 0 : (g.kv_lengths[seq] < room ? g.kv_lengths[seq] : room);
-    const int64_t place = len - (end - begin) + (token - begin);
-    int64_t last = p.causal ? (place < len - 1 ? place : len - 1) : len - 1;
-    int64_t first = p.window > 0 ? place - p.window + 1 : 0;
-    if (first < 0) first = 0;
+    const int group = p.n_q_heads / p.n_k_heads;
+    const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
+    const int seq = count_upto(g.n_seqs, token, [&](int i) { return int64_t(off(i)); });
+    if (seq >= g.n_seqs) return;
+    const int begin = off(seq), end = off(seq + 1);
+    if (token < begin || token >= end) return;
+    Plan w;
+    plan_sequence(p, w, seq, begin, end);
+    const int64_t r = int64_t(token - begin) * group + head % group;
+    w.row0 = int(r / kRowsPerBlock * kRowsPerBlock);
+    plan_keys(p, w, group, max_splits);
+    if (w.splits == 1) return;
 
-    float q[kPer], o[kPer];
-    const T *src = static_cast<const T *>(p.q) + int64_t(token) * p.q_stride + int64_t(head) * p.head_dim;
-    for (int i = 0; i < kPer; ++i) {
-        const int d = lane + i * kLanes;
-        q[i] = d < p.head_dim ? float(src[d]) : 0.0f;
-        o[i] = 0.0f;
+    float top = -INFINITY;
+    for (int i = lane; i < w.splits; i += kLanes) top = fmaxf(top, parts.stats[i * parts.rows + row].x);
+#pragma unroll
+    for (int m = 1; m < kLanes; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+    float sum = 0.0f;
+    f32x4 o = 0.0f;
+    const bool on = lane * 4 < p.head_dim;
+    for (int i = 0; i < w.splits; ++i) {
+        const float2 st = parts.stats[i * parts.rows + row];
+        if (st.y == 0.0f) continue;                     // a part that saw no key
+        const float keep = __builtin_amdgcn_exp2f(st.x == -INFINITY ? 0.0f : st.x - top);
+        sum += st.y * keep;
+        if (on)
+            o += *reinterpret_cast<const f32x4 *>(parts.o + (i * parts.rows + row) * p.head_dim +
+                                                  lane * 4) * keep;
     }
-    float top = -INFINITY, sum = 0.0f;
-    const float c = p.scale * g.k_scale * kLog2e;
-    for (int64_t j = first; j <= last; ++j) {
-        const int page = g.block_table[int64_t(seq) * g.max_pages + (j >> g.page_shift)];
-        if (page < 0 || page >= g.n_pages) continue;
-        const int64_t at = (((int64_t(page) * p.n_k_heads + kv_head) << g.page_shift) +
-                            (j & ((1 << g.page_shift) - 1))) * p.head_dim;
-        float s = 0.0f;
-        for (int i = 0; i < kPer; ++i) {
-            const int d = lane + i * kLanes;
-            if (d < p.head_dim) s = fmaf(q[i], element<CDT>(g.k_cache, at + d), s);
-        }
-        for (int m = 32; m > 0; m /= 2) s += __shfl_xor(s, m);
-        s *= c;
-        const float new_top = fmaxf(top, s);
-        const float base = new_top == -INFINITY ? 0.0f : new_top;
-        const float keep = exp2f(top - base), w = exp2f(s - base);
-        top = new_top;
-        sum = sum * keep + w;
-        for (int i = 0; i < kPer; ++i) {
-            const int d = lane + i * kLanes;
-            if (d < p.head_dim) o[i] = fmaf(w, element<CDT>(g.v_cache, at + d), o[i] * keep);
-        }
-    }
-    const float f = sum == 0.0f ? 0.0f : g.v_scale / sum;
-    T *dst = static_cast<T *>(p.out) + int64_t(token) * p.out_stride + int64_t(head) * p.head_dim;
-    for (int i = 0; i < kPer; ++i) {
-        const int d = lane + i * kLanes;
-        if (d < p.head_dim) dst[d] = T(o[i] * f);
-    }
+    if (!on) return;
+    o *= sum == 0.0f ? 0.0f : g.v_scale / sum;
+    store4<DT>(static_cast<T *>(p.out) + int64_t(token) * p.out_stride +
+                   int64_t(head) * p.head_dim + lane * 4, o);
+}
+
+// Parts of the launch: tiles of 128 rows (an upper bound that needs no look
+// at the offsets) and splits of the keys.
+struct Shape { int64_t tiles; int splits; };
+
+Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_heads,
+               int32_t page_size, int32_t max_pages)
+{
+    const int64_t group = n_q_heads / n_k_heads;
+    Shape s;
+    s.tiles = n_tokens * group / kRowsPerBlock + n_seqs;
+    const int64_t blocks = s.tiles * n_k_heads;
+    const int64_t units = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
+    const bool few_rows = n_tokens * group <= int64_t(n_seqs) * kRowsPerWave;
+    int64_t n = blocks > 0 ? (few_rows ? 4096 : 1024) / blocks : 1;
+    const int64_t most = (units + kMinUnits - 1) / kMinUnits;
+    n = n < most ? n : most;
+    n = n < 256 ? n : 256;
+    s.splits = int(n < 1 ? 1 : n);
+    return s;
+}
+
+size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int DT, int CDT>
+void launch_attend(const AttnParams &p, const Parts &parts, const Shape &s, hipStream_t stream)
+{
+    const dim3 grid(uint32_t(s.tiles * p.n_k_heads), uint32_t(s.splits));
+    const int tiles = int(s.tiles);
+    const int d = p.head_dim;
+    if (d <= 32) attend<DT, CDT, 32><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else if (d <= 64) attend<DT, CDT, 64><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else if (d <= 80) attend<DT, CDT, 80><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else if (d <= 96) attend<DT, CDT, 96><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else if (d <= 128) attend<DT, CDT, 128><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else if (d <= 192) attend<DT, CDT, 192><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    else attend<DT, CDT, 256><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t)
+size_t attention_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads,
+                                 int32_t n_k_heads, int32_t head_dim, int32_t page_size,
+                                 int32_t max_pages)
 {
-    return 256;
+    const Shape s = shape_of(n_tokens, n_seqs, n_q_heads, n_k_heads, page_size, max_pages);
+    if (s.splits == 1) return 256;
+    const size_t rows = size_t(n_tokens) * n_q_heads;
+    return round_up(s.splits * rows * sizeof(float2)) + s.splits * rows * head_dim * sizeof(float);
 }
 
 hipError_t run_paged_attention(const AttnParams &p, hipStream_t stream)
 {
-    const int64_t rows = int64_t(p.n_tokens) * p.n_q_heads;
-    const uint32_t blocks = uint32_t((rows + kWavesPerBlock - 1) / kWavesPerBlock);
+    const Shape s = shape_of(p.n_tokens, p.paged.n_seqs, p.n_q_heads, p.n_k_heads,
+                             1 << p.paged.page_shift, p.paged.max_pages);
+    Parts parts;
+    parts.rows = int64_t(p.n_tokens) * p.n_q_heads;
+    parts.stats = static_cast<float2 *>(p.workspace);
+    parts.o = reinterpret_cast<float *>(static_cast<char *>(p.workspace) +
+                                        round_up(s.splits * parts.rows * sizeof(float2)));
     const bool e4m3 = p.paged.cache_dtype == kE4M3;
-    if (p.dtype == kF16 && !e4m3)
-        attend_rows<kF16, kF16><<<blocks, kBlock, 0, stream>>>(p);
-    else if (p.dtype == kF16)
-        attend_rows<kF16, kE4M3><<<blocks, kBlock, 0, stream>>>(p);
-    else if (!e4m3)
-        attend_rows<kBF16, kBF16><<<blocks, kBlock, 0, stream>>>(p);
-    else
-        attend_rows<kBF16, kE4M3><<<blocks, kBlock, 0, stream>>>(p);
+    if (p.dtype == kF16 && !e4m3) launch_attend<kF16, kF16>(p, parts, s, stream);
+    else if (p.dtype == kF16) launch_attend<kF16, kE4M3>(p, parts, s, stream);
+    else if (!e4m3) launch_attend<kBF16, kBF16>(p, parts, s, stream);
+    else launch_attend<kBF16, kE4M3>(p, parts, s, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || s.splits == 1) return e;
+    const uint32_t blocks = uint32_t((parts.rows + kWavesPerBlock - 1) / kWavesPerBlock);
+    if (p.dtype == kF16) attend_join<kF16><<<blocks, kBlock, 0, stream>>>(p, parts, s.splits);
+    else attend_join<kBF16><<<blocks, kBlock, 0, stream>>>(p, parts, s.splits);
     return hipGetLastError();
 }
 

@@ -114,7 +114,7 @@ int check_paged(int32_t dtype, int32_t n_k_heads, int64_t n_tokens,
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
         return BEVPOOL_ERR_UNSUPPORTED;
     if (n_k_heads <= 0 || n_seqs < 0 || max_pages < 0 || n_pages <= 0) return BEVPOOL_ERR_INVALID_ARG;
-    if (n_seqs > (1 << 24) || n_pages > kInt32Limit || int64_t(max_pages) * page_size > kInt32Limit ||
+    if (n_seqs > (1 << 24) || n_pages > kInt32Limit || int64_t(max_pages) * page_size > (1 << 30) ||
         int64_t(n_seqs) * max_pages > kInt32Limit || n_pages * page_size > kInt32Limit)
         return BEVPOOL_ERR_OVERFLOW;
     if (cache_dtype == BEVPOOL_FP8_E4M3 && (!good_cache_scale(k_scale) || !good_cache_scale(v_scale)))
@@ -290,6 +290,17 @@ int bevpool_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_
     return status_of(run_kv_append(a, stream));
 }
 
+namespace {
+
+// A launch counts its blocks in 24 bits: one for every 128 rows of a key
+// head, and one for every sequence and key head.
+bool too_many_blocks(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_heads)
+{
+    return (n_tokens * (n_q_heads / n_k_heads) / 128 + n_seqs) * n_k_heads >= (1 << 24);
+}
+
+}  // namespace
+
 size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
                                               int32_t n_q_heads, int32_t n_k_heads,
                                               int32_t head_dim, int32_t page_size,
@@ -298,7 +309,8 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
     if (check_sizes(n_tokens, n_q_heads, n_k_heads, head_dim) != BEVPOOL_OK || n_seqs < 0 ||
         n_q_heads <= 0 || n_k_heads <= 0 || n_q_heads % n_k_heads != 0 || max_pages < 0 ||
         n_seqs > (1 << 24) || page_size < 16 || page_size > 256 ||
-        (page_size & (page_size - 1)) != 0 || int64_t(max_pages) * page_size > kInt32Limit)
+        (page_size & (page_size - 1)) != 0 || int64_t(max_pages) * page_size > (1 << 30) ||
+        too_many_blocks(n_tokens, n_seqs, n_q_heads, n_k_heads))
         return 0;
     return attention_workspace_bytes(n_tokens, n_seqs, n_q_heads, n_k_heads, head_dim, page_size,
                                      max_pages);
@@ -323,6 +335,7 @@ int bevpool_paged_attention(const void *q, int64_t q_stride, int32_t dtype, int6
     if (n_q_heads <= 0 || n_q_heads % n_k_heads != 0 || !good_scale(scale) ||
         !good_scale(scale * p.paged.k_scale) || window < 0 || (causal != 0 && causal != 1))
         return BEVPOOL_ERR_INVALID_ARG;
+    if (too_many_blocks(n_tokens, n_seqs, n_q_heads, n_k_heads)) return BEVPOOL_ERR_OVERFLOW;
     if (n_tokens == 0 || n_seqs == 0) return BEVPOOL_OK;
     if ((st = check_rows(q, q_stride, n_q_heads, head_dim, 2)) != BEVPOOL_OK ||
         (st = check_rows(out, out_stride, n_q_heads, head_dim, 2)) != BEVPOOL_OK)

@@ -418,8 +418,8 @@ int bevpool_qk_norm_rope_backward(const void *dq_out, int64_t dq_out_stride, con
  *       p % page_size of page block_table[s][p / page_size].  An entry outside
  *       [0, n_pages) is no page: its places hold no key (a cache may drop
  *       pages that left the window, and mark them -1).
- * n_seqs is at most 2^24; n_seqs * max_pages, max_pages * page_size and
- * n_pages * page_size stay below 2^31 (else OVERFLOW).
+ * n_seqs is at most 2^24, max_pages * page_size at most 2^30; n_seqs *
+ * max_pages and n_pages * page_size stay below 2^31 (else OVERFLOW).
  * Offsets are clipped to [0, n_tokens] and lengths to
  * [0, max_pages * page_size], so no value of these arrays makes a call read
  * or write outside its tensors.
@@ -478,7 +478,8 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
  *   workspace: at least bevpool_paged_attention_workspace_size() bytes,
  *       256-byte aligned, contents on entry ignored; calls that may overlap
  *       in time need one each.
- * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, WORKSPACE, HIP.
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW (also n_tokens * n_q_heads / 128 +
+ * n_seqs * n_k_heads from 2^24 on), WORKSPACE, HIP.
  */
 int bevpool_paged_attention(const void *q, int64_t q_stride, int32_t dtype, int64_t n_tokens,
                             int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,

@@ -85,6 +85,9 @@ class Rope:
             raise ValueError("inv_freq without sections")
         object.__setattr__(self, "sections", sections)
         object.__setattr__(self, "_h_sections", (ctypes.c_int32 * max(len(sections), 1))(*sections))
+        if sections:
+            object.__setattr__(self, "_device", self.inv_freq.get_device())
+            object.__setattr__(self, "_freq", self.inv_freq.data_ptr())
 
 
 @dataclasses.dataclass(frozen=True)
@@ -142,18 +145,22 @@ class PagedBatch:
 
 
 # ---- checks ---------------------------------------------------------------------------------
+# These run on every call of kernels that take a few microseconds, so they
+# touch each tensor as little as they can.
 def _token_rows(name, t, like=None):
     # A token tensor [n_tokens, heads, head_dim]; returns its token stride.
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n_tokens, heads, head_dim], got {tuple(t.shape)}")
-    n, heads, dim = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [n_tokens, heads, head_dim], got {tuple(shape)}")
+    n, heads, dim = shape
     if like is not None:
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if n != like.shape[0] or dim != like.shape[2]:
-            raise ValueError(f"{name} {tuple(t.shape)} does not fit {tuple(like.shape)}")
+        want = like.shape
+        if n != want[0] or dim != want[2]:
+            raise ValueError(f"{name} {tuple(shape)} does not fit {tuple(want)}")
         if t.get_device() != like.get_device():
             raise ValueError(f"{name} lies on another device")
     st, sh, sd = t.stride()
@@ -163,48 +170,49 @@ def _token_rows(name, t, like=None):
 
 
 def _output(name, out, like):
+    # The output and its token stride; a new one is contiguous.
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device), \
-            like.shape[1] * like.shape[2]
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return out, like.shape[1] * like.shape[2]
     if isinstance(out, torch.Tensor) and out.shape != like.shape:
         raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(out.shape)}")
     return out, _token_rows(name, out, like)
 
 
-def _weights(x, q_weight, k_weight):
-    # (q pointer, k pointer, dtype code) of the norm weights
-    code, ptrs = _TOKEN_DTYPE.get(x.dtype, -1), []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            ptrs.append(None)
-            continue
-        _check_device_tensor(name, w)
-        if w.numel() != x.shape[2]:
-            raise ValueError(f"{name} must have {x.shape[2]} entries")
-        if w.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"{name} must be {x.dtype} or float32, got {w.dtype}")
-        if w.get_device() != x.get_device():
-            raise ValueError(f"{name} lies on another device")
-        code = _TOKEN_DTYPE[w.dtype]
-        ptrs.append(w.data_ptr())
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must have one dtype")
-    return ptrs[0], ptrs[1], code
+def _small(name, t, x, dtype, shape):
+    # A contiguous tensor beside the tokens x; returns its address.
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != x.get_device():
+        raise ValueError(f"{name} lies on another device")
+    return t.data_ptr()
 
 
 def _rope_args(x, positions, rope, q_weight, k_weight, eps):
+    n, _, dim = x.shape
+    code, qp, kp = -1, None, None
+    if q_weight is not None or k_weight is not None:
+        dtype = (k_weight if q_weight is None else q_weight).dtype
+        if dtype is not x.dtype and dtype is not torch.float32:
+            raise TypeError(f"weights must be {x.dtype} or float32, got {dtype}")
+        code = _TOKEN_DTYPE[dtype]
+        if q_weight is not None:
+            qp = _small("q_weight", q_weight, x, dtype, (dim,))
+        if k_weight is not None:
+            kp = _small("k_weight", k_weight, x, dtype, (dim,))
     if rope is None or not rope.sections:
-        turn = (None, 0, None, None, ROPE_HALVES)
-    else:
-        _check_device_tensor("positions", positions, torch.int32)
-        want = (len(rope.sections), x.shape[0])
-        if positions.shape != want and not (want[0] == 1 and positions.shape == want[1:]):
-            raise ValueError(f"positions must be {list(want)}, got {list(positions.shape)}")
-        if positions.get_device() != x.get_device() or rope.inv_freq.get_device() != x.get_device():
-            raise ValueError("positions or inv_freq lie on another device")
-        turn = (positions.data_ptr(), len(rope.sections), rope._h_sections,
-                rope.inv_freq.data_ptr(), rope.layout)
-    return (*_weights(x, q_weight, k_weight), float(eps), *turn)
+        return qp, kp, code, eps, None, 0, None, None, ROPE_HALVES
+    if rope._device != x.get_device():
+        raise ValueError("inv_freq lies on another device")
+    axes = len(rope.sections)
+    want = (n,) if axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 1 \
+        else (axes, n)
+    pos = _small("positions", positions, x, torch.int32, want)
+    return qp, kp, code, eps, pos, axes, rope._h_sections, rope._freq, rope.layout
 
 
 def _paged_args(x, cache, batch):
@@ -238,6 +246,16 @@ def _tensors(args):
             yield a.inv_freq
 
 
+try:
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+    from torch._C import _cuda_getDevice as _current_device
+except ImportError:                      # a torch built without GPU support
+    def _current_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+    _current_device = torch.cuda.current_device
+
+
 def _on_device(call):
     """Runs call with its first tensor's device current and, where stream is
     given, with that stream current; the arguments are then marked as used on
@@ -247,7 +265,7 @@ def _on_device(call):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("the first argument must be a GPU tensor")
         if stream is None:
-            if first.get_device() == torch.cuda.current_device():
+            if first.get_device() == _current_device():
                 return call(first, *args, **kw)
             with torch.cuda.device(first.device):
                 return call(first, *args, **kw)
@@ -261,8 +279,9 @@ def _on_device(call):
     return run
 
 
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
+def _raw_stream(t):
+    # the handle of the current stream of t's device, without a Stream object
+    return _current_stream(t.get_device())
 
 
 # ---- calls ----------------------------------------------------------------------------------
@@ -296,7 +315,7 @@ def bevpool_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     rc = lib.bevpool_qk_norm_rope(
         q.data_ptr(), sq, kp, sk, _TOKEN_DTYPE[q.dtype], n, hq, hk, dim,
         *_rope_args(q, positions, rope, q_weight, k_weight, eps), q_out.data_ptr(), sqo, ko, sko,
-        _raw_stream())
+        _raw_stream(q))
     if rc != OK:
         raise BevPoolError("bevpool_qk_norm_rope", rc)
     return q_out, k_out
@@ -324,7 +343,7 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
     bevpool_qk_norm_rope_backward_workspace_size bytes; made here when None.
     Keyword stream: where to run."""
     lib = _lib()
-    sg = _token_rows("dq_out", dq_out)
+    _token_rows("dq_out", dq_out)
     n, hq, dim = dq_out.shape
     if dq_out.dtype not in _TOKEN_DTYPE:
         raise TypeError(f"dq_out must be float32, float16 or bfloat16, got {dq_out.dtype}")
@@ -355,9 +374,9 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
     dqw, dkw = (None if w is None else torch.empty(dim, dtype=torch.float32, device=dq_out.device)
                 for w in (q_weight, k_weight))
     rc = lib.bevpool_qk_norm_rope_backward(
-        gq, sg, gk, sgk, xq, sxq, xk, sxk, _TOKEN_DTYPE[dq_out.dtype], n, hq, hk, dim, *rope_args,
+        gq, sgq, gk, sgk, xq, sxq, xk, sxk, _TOKEN_DTYPE[dq_out.dtype], n, hq, hk, dim, *rope_args,
         pdq, sdq, pdk, sdk, None if dqw is None else dqw.data_ptr(),
-        None if dkw is None else dkw.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream())
+        None if dkw is None else dkw.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dq_out))
     if rc != OK:
         raise BevPoolError("bevpool_qk_norm_rope_backward", rc)
     return dq, dk, dqw, dkw
@@ -396,7 +415,7 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
     rc = lib.bevpool_kv_append(
         qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, _TOKEN_DTYPE[k.dtype], n, hq, hk, dim,
         *_rope_args(k, positions, rope, q_weight, k_weight, eps), qo, sqo,
-        *_paged_args(k, cache, batch), _raw_stream())
+        *_paged_args(k, cache, batch), _raw_stream(k))
     if rc != OK:
         raise BevPoolError("bevpool_kv_append", rc)
     return q_out
@@ -435,7 +454,7 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
     rc = lib.bevpool_paged_attention(
         q.data_ptr(), sq, _TOKEN_DTYPE[q.dtype], n, hq, hk, dim, *paged,
         dim ** -0.5 if scale is None else float(scale), int(causal), int(window), out.data_ptr(),
-        so, ws.data_ptr(), ws.numel(), _raw_stream())
+        so, ws.data_ptr(), ws.numel(), _raw_stream(q))
     if rc != OK:
         raise BevPoolError("bevpool_paged_attention", rc)
     return out

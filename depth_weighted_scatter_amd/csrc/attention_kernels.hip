@@ -31,7 +31,7 @@ constexpr int kWavesPerBlock = kBlock / kLanes;
 constexpr int kRowsPerWave = 32;
 constexpr int kRowsPerBlock = kWavesPerBlock * kRowsPerWave;
 constexpr int kUnit = 128;            // keys: ranges of a split are multiples of this
-constexpr int kMinUnits = 4;          // and at least this many
+constexpr int kMinUnits = 2;          // and at least this many
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -138,6 +138,25 @@ __device__ __forceinline__ void plan_sequence(const AttnParams &p, Plan &w, int 
     w.len = len < 0 ? 0 : (len < room ? len : int(room));
 }
 
+// The sequence and first row of a tile, by the whole wave.  The tiles of
+// sequence s start at off(s) * G / 128 + s: each has room for all of its rows,
+// and the start grows with s.  Fills in w up to row0; false for a tile that is
+// nobody's.
+__device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile, int group)
+{
+    const PagedParams &g = p.paged;
+    const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
+    const auto start = [&](int i) { return int64_t(off(i)) * group / kRowsPerBlock + i; };
+    const int seq = count_upto(g.n_seqs, tile, start);
+    if (seq >= g.n_seqs) return false;
+    const int begin = off(seq), end = off(seq + 1);
+    const int64_t row0 = (tile - start(seq)) * kRowsPerBlock;
+    if (row0 < 0 || row0 >= int64_t(end - begin) * group) return false;
+    plan_sequence(p, w, seq, begin, end);
+    w.row0 = int(row0);
+    return true;
+}
+
 // One wave's rows: their part of O^T, running maximum of the scores (before
 // the scale) and this lane's part of the weights' sum.
 template <int DP> struct Rows {
@@ -197,17 +216,30 @@ __device__ __forceinline__ u32x4 widen(u32x2 raw)
 __device__ const u32x4 kZeroPiece = {0, 0, 0, 0};
 
 // One 16-byte piece for each lane, straight from memory to LDS: lane i's goes
-// to lds + 16 i.  Not seen by the compiler's wait counts: a wait_loads<n>
-// before the data is used is the caller's.
-__device__ __forceinline__ void load_to_lds(const void *from, const char *lds)
+// to LDS address at + 16 i.  Not seen by the compiler's wait counts: a
+// wait_loads<n> before the data is used is the caller's.  An M0 write and the
+// load that uses it need a wait state between them.
+__device__ __forceinline__ void load_to_lds(const void *from, uint32_t at)
 {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(
-        uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)lds)));
-    // an M0 write and the load that uses it need a wait state between them
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                  :
                  : "v"(from), "s"(at)
                  : "memory");
+}
+
+// The same from a uniform base and a lane's byte offset.
+__device__ __forceinline__ void load_to_lds(const void *base, uint32_t offset, uint32_t at)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
+                 :
+                 : "s"(base), "v"(offset), "s"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const char *p)
+{
+    return __builtin_amdgcn_readfirstlane(
+        uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)p)));
 }
 
 // Waits until at most N of the wave's memory reads are pending (they complete
@@ -221,96 +253,109 @@ __device__ __forceinline__ void wait_loads()
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
 // Brings tiles of KEYS keys to LDS.  The keys of a tile are 16-key groups, each
-// on one page; lane i of a wave keeps the page of the i-th group to come, 64
-// groups at a time.  Groups on no page, or past `end`, are read from page 0
-// and hidden later, so every read is inside the cache.
+// on one page; lane i of a wave keeps the place in the cache of the i-th group
+// to come, 64 groups at a time.  Groups on no page, or past `end`, are read
+// from page 0 and hidden later, so every read is inside the cache.
 //
 // WAVES waves share a tile; 16-bit caches go straight to LDS, e4m3 ones are
 // read into registers (fetch) and widened on the way to LDS (store).
 template <int DT, int CDT, int DP, int KEYS, int WAVES>
 struct Stage {
     using L = Tiles<DP>;
+    using C = typename Elem<CDT>::type;
     static constexpr int VT = Types<DT, CDT>::V;
     static constexpr bool kDirect = CDT != kE4M3;
     static constexpr int kGroups = KEYS / 16;
     static constexpr int kLoads = KEYS * L::kPieces / kLanes;       // 64-lane loads of a tile
     static constexpr int kSlots = (kLoads + WAVES - 1) / WAVES;     // of them, a wave's
-    static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of pages
-    using C = typename Elem<CDT>::type;
+    static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of groups
+    // a load stays within one group, or reaches into the next
+    static constexpr bool kOneGroup = L::kPieces % 4 == 0;
 
     const AttnParams &p;
     const int32_t *table;
     int kv_head, wave, end, first, stride;     // tile t holds keys first + t * stride ...
-    int pages;                                 // lane's group's page, -1 for none
+    int row_bytes;
+    uint32_t group_lo, group_hi;               // lane's group: its byte offset in the cache
+    uint64_t have;                             // groups that are on a page
+    int offset[2][kSlots];                     // lane's pieces: bytes from their group, -1 for a zero
     u32x2 k[kDirect ? 1 : kSlots], v[kDirect ? 1 : kSlots];
 
     __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
                      int stride, int end)
         : p(p), table(p.paged.block_table + int64_t(w.seq) * p.paged.max_pages), kv_head(kv_head),
-          wave(wave), end(end), first(first), stride(stride)
+          wave(wave), end(end), first(first), stride(stride),
+          row_bytes(p.head_dim * int(sizeof(C)))
     {
+#pragma unroll
+        for (int n = 0; n < kSlots; ++n) {
+            const int id = (n * WAVES + wave) * kLanes + (int(threadIdx.x) & (kLanes - 1));
+            const int key = id / L::kPieces, at = id % L::kPieces;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int piece = at ^ (i ? L::value_swizzle(key) : L::key_swizzle(key));
+                offset[i][n] = piece * 8 < p.head_dim
+                                   ? key % 16 * row_bytes + piece * 8 * int(sizeof(C)) : -1;
+            }
+        }
     }
 
     __device__ __forceinline__ void find_pages(int tile)
     {
+        const PagedParams &g = p.paged;
         const int lane = int(threadIdx.x) & (kLanes - 1);
         const int64_t key = first + int64_t(tile + lane / kGroups) * stride + lane % kGroups * 16;
-        pages = -1;
-        if (key < end) pages = table[key >> p.paged.page_shift];
-        if (pages >= p.paged.n_pages) pages = -1;
+        int page = -1;
+        if (key < end) page = table[key >> g.page_shift];
+        if (page >= g.n_pages) page = -1;
+        have = __ballot(page >= 0);
+        const int64_t row = ((int64_t(max(page, 0)) * p.n_k_heads + kv_head) << g.page_shift) +
+                            (key & ((1 << g.page_shift) - 1));
+        const uint64_t at = uint64_t(row) * uint32_t(row_bytes);
+        group_lo = uint32_t(at);
+        group_hi = uint32_t(at >> 32);
     }
 
     // One bit for each 16-key group of the tile that is on a page.
     __device__ __forceinline__ uint32_t groups_there(int tile) const
     {
-        return uint32_t(__ballot(pages >= 0) >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
+        return uint32_t(have >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
     }
 
-    // First element of the tile's group in the cache.
-    __device__ __forceinline__ int64_t group_at(int tile, int group) const
+    __device__ __forceinline__ const char *group_at(const void *cache, int tile, int group) const
     {
-        const PagedParams &g = p.paged;
-        const int page = max(__builtin_amdgcn_readlane(pages, tile % kBatch * kGroups + group), 0);
-        const int key = first + tile * stride + group * 16;
-        return (((int64_t(page) * p.n_k_heads + kv_head) << g.page_shift) +
-                (key & ((1 << g.page_shift) - 1))) * p.head_dim;
+        const int lane = tile % kBatch * kGroups + group;
+        const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), lane));
+        const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), lane));
+        return static_cast<const char *>(cache) + (hi << 32 | lo);
     }
 
-    // This lane's piece of load m: its address in the cache and its key.
+    // Issues a tile's reads of keys or of values (to LDS address lds).
     template <bool VALUES>
-    __device__ __forceinline__ const C *source(const int64_t (&at)[kGroups], int m, int &key) const
+    __device__ __forceinline__ void fetch(int tile, uint32_t lds)
     {
-        const int id = m * kLanes + (int(threadIdx.x) & (kLanes - 1));
-        key = id / L::kPieces;
-        const int piece = (id % L::kPieces) ^ (VALUES ? L::value_swizzle(key) : L::key_swizzle(key));
-        int64_t base;
-        if constexpr (L::kPieces % 4 == 0) {          // a load stays within one group
-            base = at[m / (L::kPieces / 4)];
-        } else {
-            base = at[0];
-#pragma unroll
-            for (int i = 1; i < kGroups; ++i) base = key / 16 == i ? at[i] : base;
-        }
-        const C *cache = static_cast<const C *>(VALUES ? p.paged.v_cache : p.paged.k_cache);
-        const C *from = cache + base + (key % 16) * p.head_dim + piece * 8;
-        if (DP != p.head_dim && piece * 8 >= p.head_dim)
-            from = reinterpret_cast<const C *>(&kZeroPiece);
-        return from;
-    }
-
-    // Issues a tile's reads of keys or of values.
-    template <bool VALUES>
-    __device__ __forceinline__ void fetch(int tile, const char *lds)
-    {
-        int64_t at[kGroups];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) at[i] = group_at(tile, i);
+        const void *cache = VALUES ? p.paged.v_cache : p.paged.k_cache;
+        const bool exact = p.head_dim == DP;
 #pragma unroll
         for (int n = 0; n < kSlots; ++n) {
             const int m = n * WAVES + wave;
             if (kLoads % WAVES != 0 && m >= kLoads) continue;
-            int key;
-            const C *from = source<VALUES>(at, m, key);
+            const int group = m * kLanes / L::kPieces / 16;
+            const char *base = group_at(cache, tile, group);
+            const int off = offset[VALUES][n];
+            if (kOneGroup && exact) {
+                if constexpr (kDirect) load_to_lds(base, uint32_t(off), lds + m * 1024);
+                else (VALUES ? v : k)[n] = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
+                continue;
+            }
+            const char *from = base + off;
+            if constexpr (!kOneGroup) {
+                const int next = min(group + 1, kGroups - 1);
+                const int key = (m * kLanes + (int(threadIdx.x) & (kLanes - 1))) / L::kPieces;
+                const char *other = group_at(cache, tile, next) + off;
+                from = key / 16 == group ? from : other;
+            }
+            if (!exact && off < 0) from = reinterpret_cast<const char *>(&kZeroPiece);
             if constexpr (kDirect) load_to_lds(from, lds + m * 1024);
             else (VALUES ? v : k)[n] = *reinterpret_cast<const u32x2 *>(from);
         }
@@ -355,23 +400,42 @@ struct Stage {
     }
 };
 
-// S^T of one tile for a wave's rows.
+// S^T of one tile for a wave's rows.  The operands are read a batch ahead of
+// the matrix instructions that use them, and the barriers keep it so: left
+// alone, the compiler puts each read right before its use, and the wave waits
+// out the latency of LDS every time.
 template <int DT, int DP, int KT>
 __device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<DP>::kSteps],
                                        const char *keys)
 {
     using L = Tiles<DP>;
+    constexpr int kReads = KT * L::kSteps, kBatch = 8, kBatches = (kReads + kBatch - 1) / kBatch;
     const int lane = int(threadIdx.x) & (kLanes - 1);
     const int col = lane & 31, piece = (lane >> 5) ^ L::key_swizzle(col);
     const char *row = keys + col * L::kRow;
+    u32x4 a[2][kBatch];
+    const auto read = [&](int batch) {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-        s[kt] = 0.0f;
+        for (int i = 0; i < kBatch; ++i) {
+            const int n = batch * kBatch + i;
+            if (n < kReads)
+                a[batch & 1][i] = *reinterpret_cast<const u32x4 *>(
+                    row + n / L::kSteps * 32 * L::kRow + ((piece ^ (2 * (n % L::kSteps))) << 4));
+        }
+    };
 #pragma unroll
-        for (int st = 0; st < L::kSteps; ++st)
-            s[kt] = mfma<DT>(*reinterpret_cast<const u32x4 *>(row + kt * 32 * L::kRow +
-                                                              ((piece ^ (2 * st)) << 4)),
-                             q[st], s[kt]);
+    for (int kt = 0; kt < KT; ++kt) s[kt] = 0.0f;
+    read(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int batch = 0; batch < kBatches; ++batch) {
+        if (batch + 1 < kBatches) read(batch + 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int n = batch * kBatch + i;
+            if (n < kReads) s[n / L::kSteps] = mfma<DT>(a[batch & 1][i], q[n % L::kSteps], s[n / L::kSteps]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -380,12 +444,16 @@ __device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<D
 template <int KT>
 __device__ __forceinline__ void hide(f32x16 (&s)[KT], int lo, int hi, uint32_t there)
 {
+    // register i holds key kt * 32 + 8 (i / 4) + i % 4 + 4 half; the half goes
+    // to the limits, so that the rest is a constant
     const int half = (int(threadIdx.x) & (kLanes - 1)) >> 5;
+    lo -= 4 * half;
+    hi -= 4 * half;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int key = kt * 32 + 8 * (i / 4) + 4 * half + i % 4;
+            const int key = kt * 32 + 8 * (i / 4) + i % 4;
             const bool seen = key >= lo && key < hi && ((there >> (kt * 2 + i / 8)) & 1);
             s[kt][i] = seen ? s[kt][i] : -INFINITY;
         }
@@ -429,9 +497,11 @@ __device__ __forceinline__ void weights(Rows<DP> &r, f32x16 (&s)[KT], u32x4 (&w)
     }
 }
 
-// O^T += V^T P^T.
-template <int VT, int DP, int KT>
-__device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT], const char *values)
+// Operands of O^T for 16 keys: V^T, 32 dims each.
+template <int DP> struct Values { u32x4 a[Tiles<DP>::kDims]; };
+
+template <int DP>
+__device__ __forceinline__ Values<DP> read_values(const char *values, int u)
 {
     using L = Tiles<DP>;
     using Lds = __attribute__((address_space(3))) i16x4;
@@ -441,16 +511,32 @@ __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT]
     const int in_row = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     const int swizzle = L::value_swizzle(key) >> 2;
     const char *from = values + key * L::kRow + in_row;
+    Values<DP> x;
 #pragma unroll
-    for (int u = 0; u < KT * 2; ++u)
+    for (int dt = 0; dt < L::kDims; ++dt) {
+        const char *at = from + u * 16 * L::kRow + ((dt ^ swizzle) << 6);
+        const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)at);
+        const i16x4 z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at + 8 * L::kRow));
+        const u32x2 yy = __builtin_bit_cast(u32x2, y), zz = __builtin_bit_cast(u32x2, z);
+        x.a[dt] = u32x4{yy.x, yy.y, zz.x, zz.y};
+    }
+    return x;
+}
+
+// O^T += V^T P^T; ready: the operands of the tile's first 16 keys.
+template <int VT, int DP, int KT>
+__device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT], const char *values,
+                                           Values<DP> ready)
+{
 #pragma unroll
-        for (int dt = 0; dt < L::kDims; ++dt) {
-            const char *at = from + u * 16 * L::kRow + ((dt ^ swizzle) << 6);
-            const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)at);
-            const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at + 8 * L::kRow));
-            const u32x2 xx = __builtin_bit_cast(u32x2, x), yy = __builtin_bit_cast(u32x2, y);
-            r.o[dt] = mfma<VT>(u32x4{xx.x, xx.y, yy.x, yy.y}, w[u], r.o[dt]);
-        }
+    for (int u = 0; u < KT * 2; ++u) {
+        Values<DP> next;
+        if (u + 1 < KT * 2) next = read_values<DP>(values, u + 1);
+#pragma unroll
+        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] = mfma<VT>(ready.a[dt], w[u], r.o[dt]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u + 1 < KT * 2) ready = next;
+    }
 }
 
 // The infinities and NaN of four dims among the values that a row sees, added
@@ -515,19 +601,8 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     const int tile = tiles - 1 - int(blockIdx.x) / p.n_k_heads;
     const int split = int(blockIdx.y);
 
-    // The sequence whose tiles include this one.  Its tiles start at
-    // off * G / 128 + seq: every sequence has room for all of its rows, and
-    // the start grows with it.
-    const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
-    const auto start = [&](int i) { return int64_t(off(i)) * group / kRowsPerBlock + i; };
-    const int seq = count_upto(g.n_seqs, tile, start);
-    if (seq >= g.n_seqs) return;
-    const int begin = off(seq), end = off(seq + 1);
-    const int64_t row0 = (tile - start(seq)) * kRowsPerBlock;
-    if (row0 < 0 || row0 >= int64_t(end - begin) * group) return;
     Plan w;
-    plan_sequence(p, w, seq, begin, end);
-    w.row0 = int(row0);
+    if (!find_tile(p, w, tile, group)) return;
     plan_keys(p, w, group, max_splits);
     if (split >= w.splits) return;
     const int from = w.lo + split * w.per;
@@ -537,7 +612,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     // this lane's row, its limits, and its queries (rows past the last repeat it)
     const int first = by_keys ? 0 : wave * kRowsPerWave;
     const int row = w.row0 + min(first + col, w.rows - 1);
-    const int token = begin + row / group, head = kv_head * group + row % group;
+    const int token = w.begin + row / group, head = kv_head * group + row % group;
     int lo, hi;
     row_limits(p, w, row, group, lo, hi);
     u32x4 q[L::kSteps];
@@ -547,6 +622,10 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
 #pragma unroll
         for (int st = 0; st < L::kSteps; ++st)
             q[st] = st * 16 < p.head_dim ? *reinterpret_cast<const u32x4 *>(src + st * 16) : u32x4(0u);
+        // wait for them here: a wait inside the loop would be one for the next
+        // tile's reads as well
+#pragma unroll
+        for (int st = 0; st < L::kSteps; ++st) asm volatile("" : "+v"(q[st]));
     }
     // limits of all of the wave's rows (they grow with the row)
     const int wave_lo = __shfl(lo, 0), wave_hi = __shfl(hi, 31);
@@ -561,6 +640,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
 #pragma unroll
     for (int dt = 0; dt < L::kDims; ++dt) r.o[dt] = 0.0f;
 
+    const uint32_t at = lds_address(lds);
     if (!by_keys) {
         // two buffers of 64 keys: a tile's reads run while the one before it
         // is worked on
@@ -575,8 +655,8 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
         const int n_tiles = (to - from + 63) / 64;
         if (n_tiles > 0) {
             st.find_pages(0);
-            st.template fetch<false>(0, lds);
-            st.template fetch<true>(0, lds + kHalf);
+            st.template fetch<false>(0, at);
+            st.template fetch<true>(0, at + kHalf);
         }
         uint32_t there = n_tiles > 0 ? st.groups_there(0) : 0;
         for (int tile = 0; tile < n_tiles; ++tile) {
@@ -593,7 +673,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             if (tile + 1 < n_tiles) {
                 if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
                 there = st.groups_there(tile + 1);
-                char *next = lds + ((tile + 1) & 1) * 2 * kHalf;
+                const uint32_t next = at + ((tile + 1) & 1) * 2 * kHalf;
                 st.template fetch<false>(tile + 1, next);
                 st.template fetch<true>(tile + 1, next + kHalf);
             }
@@ -607,8 +687,10 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
                 scores<DT, DP, 2>(s, q, keys);
                 if (key0 < all_lo || key0 + 64 > min(all_hi, to) || now != 15)
                     hide<2>(s, lo - key0, min(hi, to) - key0, now);
+                const Values<DP> ready = read_values<DP>(values, 0);
+                __builtin_amdgcn_sched_barrier(0);
                 weights<VT, DP, 2>(r, s, x, c);
-                add_values<VT, DP, 2>(r, x, values);
+                add_values<VT, DP, 2>(r, x, values, ready);
             }
         }
     } else {
@@ -620,11 +702,12 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
         const int first_key = from + wave * 32;
         S st(p, w, kv_head, 0, first_key, kStep, to);
         char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
+        const uint32_t keys_at = at + wave * 2 * kHalf, values_at = keys_at + kHalf;
         const int n_tiles = to > first_key ? (to - first_key + kStep - 1) / kStep : 0;
         if (n_tiles > 0) {
             st.find_pages(0);
-            st.template fetch<false>(0, keys);
-            st.template fetch<true>(0, values);
+            st.template fetch<false>(0, keys_at);
+            st.template fetch<true>(0, values_at);
         }
         for (int tile = 0; tile < n_tiles; ++tile) {
             const int key0 = first_key + tile * kStep;
@@ -642,8 +725,8 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             if (more) {
                 if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
                 wait_lds();
-                st.template fetch<false>(tile + 1, keys);
-                if constexpr (!S::kDirect) st.template fetch<true>(tile + 1, values);
+                st.template fetch<false>(tile + 1, keys_at);
+                if constexpr (!S::kDirect) st.template fetch<true>(tile + 1, values_at);
             }
             const bool whole = key0 >= all_lo && key0 + 32 <= min(all_hi, to) && there == 3;
             if (!whole) hide<1>(s, lo - key0, min(hi, to) - key0, there);
@@ -653,10 +736,10 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
                 else wait_loads<0>();
             }
             if (!whole) st.clean_values(values, tile, there, &bad);
-            add_values<VT, DP, 1>(r, x, values);
+            add_values<VT, DP, 1>(r, x, values, read_values<DP>(values, 0));
             if constexpr (S::kDirect) {
                 wait_lds();
-                if (more) st.template fetch<true>(tile + 1, values);
+                if (more) st.template fetch<true>(tile + 1, values_at);
             }
         }
     }
@@ -717,7 +800,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             sum = wave_stats[n / 32][n % 32][1];
         }
         const int row = w.row0 + n;
-        const int64_t t = begin + row / group;
+        const int64_t t = w.begin + row / group;
         const int h = kv_head * group + row % group;
         if (bad) {
             int lo, hi;
@@ -729,57 +812,87 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             x *= sum == 0.0f ? 0.0f : g.v_scale / sum;
             store4<DT>(static_cast<T *>(p.out) + t * p.out_stride + int64_t(h) * p.head_dim + d, x);
         } else {
-            const int64_t at = split * parts.rows + t * p.n_q_heads + h;
-            *reinterpret_cast<f32x4 *>(parts.o + at * p.head_dim + d) = x;
-            if (d == 0) parts.stats[at] = make_float2(top * c, sum);
+            const int64_t part = split * parts.rows + t * p.n_q_heads + h;
+            *reinterpret_cast<f32x4 *>(parts.o + part * p.head_dim + d) = x;
+            if (d == 0) parts.stats[part] = make_float2(top * c, sum);
         }
     }
 }
 
-// Adds the splits of a row: one wave for each (token, query head), a lane for
-// four dims.  Rows of one split are already in place.
+// Adds the splits of the rows of a tile; tiles of one split are already in
+// place.  The rows of a tile go to gridDim.y blocks in turn; a thread takes
+// four dims of a row, or, where a block has few rows, `ways` threads share the
+// splits and meet in LDS.
+constexpr int kJoinBlock = 512;
+
+struct Sum {
+    float top, sum;      // maximum * c, sum of weights
+    f32x4 o;
+};
+
+__device__ __forceinline__ float part_weight(float top, float all)
+{
+    // scores that are all NaN leave no maximum, but a sum
+    return top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - all);
+}
+
 template <int DT>
-__global__ __launch_bounds__(kBlock) void attend_join(AttnParams p, Parts parts, int max_splits)
+__global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts parts, int max_splits)
 {
     using T = typename Elem<DT>::type;
-    const PagedParams &g = p.paged;
-    const int lane = int(threadIdx.x) & (kLanes - 1);
-    const int64_t row = int64_t(blockIdx.x) * kWavesPerBlock + int(threadIdx.x) / kLanes;
-    if (row >= parts.rows) return;
-    const int token = int(row / p.n_q_heads), head = int(row % p.n_q_heads);
+    __shared__ Sum shared[kJoinBlock];
     const int group = p.n_q_heads / p.n_k_heads;
-    const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
-    const int seq = count_upto(g.n_seqs, token, [&](int i) { return int64_t(off(i)); });
-    if (seq >= g.n_seqs) return;
-    const int begin = off(seq), end = off(seq + 1);
-    if (token < begin || token >= end) return;
+    const int kv_head = int(blockIdx.x) % p.n_k_heads;
     Plan w;
-    plan_sequence(p, w, seq, begin, end);
-    const int64_t r = int64_t(token - begin) * group + head % group;
-    w.row0 = int(r / kRowsPerBlock * kRowsPerBlock);
+    if (!find_tile(p, w, int(blockIdx.x) / p.n_k_heads, group)) return;
     plan_keys(p, w, group, max_splits);
     if (w.splits == 1) return;
 
-    float top = -INFINITY;
-    for (int i = lane; i < w.splits; i += kLanes) top = fmaxf(top, parts.stats[i * parts.rows + row].x);
-#pragma unroll
-    for (int m = 1; m < kLanes; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
-    float sum = 0.0f;
-    f32x4 o = 0.0f;
-    const bool on = lane * 4 < p.head_dim;
-    for (int i = 0; i < w.splits; ++i) {
-        const float2 st = parts.stats[i * parts.rows + row];
-        if (st.y == 0.0f) continue;                     // a part that saw no key
-        const float keep = __builtin_amdgcn_exp2f(st.x == -INFINITY ? 0.0f : st.x - top);
-        sum += st.y * keep;
-        if (on)
-            o += *reinterpret_cast<const f32x4 *>(parts.o + (i * parts.rows + row) * p.head_dim +
-                                                  lane * 4) * keep;
+    const int turn = int(gridDim.y), rows = (w.rows - int(blockIdx.y) + turn - 1) / turn;
+    const int fours = p.head_dim / 4, n = rows * fours;
+    int ways = 1;
+    while (ways * 2 * n <= kJoinBlock && ways < w.splits) ways *= 2;
+    const int per_way = kJoinBlock / ways;
+    const int way = int(threadIdx.x) / per_way;
+
+    const auto row_of = [&](int i) { return w.row0 + int(blockIdx.y) + i / fours * turn; };
+    const auto put = [&](int row, int d, const Sum &a) {
+        const float f = a.sum == 0.0f ? 0.0f : p.paged.v_scale / a.sum;
+        store4<DT>(static_cast<T *>(p.out) + int64_t(w.begin + row / group) * p.out_stride +
+                       int64_t(kv_head * group + row % group) * p.head_dim + d, a.o * f);
+    };
+    for (int i = int(threadIdx.x) % per_way; i < n; i += per_way) {
+        const int row = row_of(i), d = i % fours * 4;
+        const int64_t at = int64_t(w.begin + row / group) * p.n_q_heads + kv_head * group + row % group;
+        const float2 *stats = parts.stats + at;
+        const float *o = parts.o + at * p.head_dim + d;
+        Sum a = {-INFINITY, 0.0f, f32x4(0.0f)};
+#pragma unroll 4
+        for (int k = way; k < w.splits; k += ways) a.top = fmaxf(a.top, stats[k * parts.rows].x);
+#pragma unroll 4
+        for (int k = way; k < w.splits; k += ways) {
+            const float2 st = stats[k * parts.rows];
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(o + k * parts.rows * p.head_dim);
+            const float f = st.y == 0.0f ? 0.0f : part_weight(st.x, a.top);   // 0: saw no key
+            a.sum += st.y * f;
+            a.o += x * f;
+        }
+        if (ways > 1) shared[threadIdx.x] = a;     // n <= per_way: the only turn of the loop
+        else put(row, d, a);
     }
-    if (!on) return;
-    o *= sum == 0.0f ? 0.0f : g.v_scale / sum;
-    store4<DT>(static_cast<T *>(p.out) + int64_t(token) * p.out_stride +
-                   int64_t(head) * p.head_dim + lane * 4, o);
+    if (ways == 1) return;
+    __syncthreads();
+    const int i = int(threadIdx.x);
+    if (i >= n) return;
+    Sum a = {-INFINITY, 0.0f, f32x4(0.0f)};
+    for (int k = 0; k < ways; ++k) a.top = fmaxf(a.top, shared[k * per_way + i].top);
+    for (int k = 0; k < ways; ++k) {
+        const Sum &b = shared[k * per_way + i];
+        const float f = b.sum == 0.0f ? 0.0f : part_weight(b.top, a.top);
+        a.sum += b.sum * f;
+        a.o += b.o * f;
+    }
+    put(row_of(i), i % fours * 4, a);
 }
 
 // Parts of the launch: tiles of 128 rows (an upper bound that needs no look
@@ -787,19 +900,41 @@ __global__ __launch_bounds__(kBlock) void attend_join(AttnParams p, Parts parts,
 struct Shape { int64_t tiles; int splits; };
 
 Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_heads,
-               int32_t page_size, int32_t max_pages)
+               int32_t head_dim, int32_t page_size, int32_t max_pages)
 {
     const int64_t group = n_q_heads / n_k_heads;
     Shape s;
     s.tiles = n_tokens * group / kRowsPerBlock + n_seqs;
     const int64_t blocks = s.tiles * n_k_heads;
     const int64_t units = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
-    const bool few_rows = n_tokens * group <= int64_t(n_seqs) * kRowsPerWave;
-    int64_t n = blocks > 0 ? (few_rows ? 4096 : 1024) / blocks : 1;
-    const int64_t most = (units + kMinUnits - 1) / kMinUnits;
-    n = n < most ? n : most;
-    n = n < 256 ? n : 256;
-    s.splits = int(n < 1 ? 1 : n);
+    const int64_t slots = head_dim > 128 ? 256 : 512;        // blocks the chip holds
+    s.splits = 1;
+    if (blocks == 0 || units <= 4) return s;
+    if (n_tokens * group <= int64_t(n_seqs) * kRowsPerWave) {
+        // few rows: the keys are read once and HBM decides.  Enough blocks to
+        // fill the chip, and then more while each still has 8 units, so that
+        // sequences of different lengths end together
+        int64_t n = slots / blocks;
+        if (n * kMinUnits > units) n = units / kMinUnits;
+        int64_t fine = 4096 / blocks;
+        if (fine * 8 > units) fine = units / 8;
+        n = n > fine ? n : fine;
+        n = n < 256 ? n : 256;
+        s.splits = int(n < 1 ? 1 : n);
+        return s;
+    }
+    // many rows: the blocks run in rounds of `slots`; a split costs about two
+    // units more in each block and, where there are any, four for the join
+    const int64_t full = (n_tokens * group + (n_seqs - 1) * (kRowsPerBlock / 2) + kRowsPerBlock - 1) /
+                         kRowsPerBlock * n_k_heads;        // about the tiles that have rows
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= 8 && n * kMinUnits <= units; ++n) {
+        const int64_t cost = (full * n + slots - 1) / slots * ((units + n - 1) / n + 2) + (n > 1 ? 4 : 0);
+        if (cost < best) {
+            best = cost;
+            s.splits = n;
+        }
+    }
     return s;
 }
 
@@ -826,7 +961,8 @@ size_t attention_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_h
                                  int32_t n_k_heads, int32_t head_dim, int32_t page_size,
                                  int32_t max_pages)
 {
-    const Shape s = shape_of(n_tokens, n_seqs, n_q_heads, n_k_heads, page_size, max_pages);
+    const Shape s = shape_of(n_tokens, n_seqs, n_q_heads, n_k_heads, head_dim, page_size,
+                             max_pages);
     if (s.splits == 1) return 256;
     const size_t rows = size_t(n_tokens) * n_q_heads;
     return round_up(s.splits * rows * sizeof(float2)) + s.splits * rows * head_dim * sizeof(float);
@@ -834,7 +970,7 @@ size_t attention_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t n_q_h
 
 hipError_t run_paged_attention(const AttnParams &p, hipStream_t stream)
 {
-    const Shape s = shape_of(p.n_tokens, p.paged.n_seqs, p.n_q_heads, p.n_k_heads,
+    const Shape s = shape_of(p.n_tokens, p.paged.n_seqs, p.n_q_heads, p.n_k_heads, p.head_dim,
                              1 << p.paged.page_shift, p.paged.max_pages);
     Parts parts;
     parts.rows = int64_t(p.n_tokens) * p.n_q_heads;
@@ -848,9 +984,9 @@ hipError_t run_paged_attention(const AttnParams &p, hipStream_t stream)
     else launch_attend<kBF16, kE4M3>(p, parts, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1) return e;
-    const uint32_t blocks = uint32_t((parts.rows + kWavesPerBlock - 1) / kWavesPerBlock);
-    if (p.dtype == kF16) attend_join<kF16><<<blocks, kBlock, 0, stream>>>(p, parts, s.splits);
-    else attend_join<kBF16><<<blocks, kBlock, 0, stream>>>(p, parts, s.splits);
+    const dim3 blocks(uint32_t(s.tiles * p.n_k_heads), s.splits >= 16 ? 8 : 1);
+    if (p.dtype == kF16) attend_join<kF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.splits);
+    else attend_join<kBF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.splits);
     return hipGetLastError();
 }
 

@@ -252,25 +252,27 @@ __device__ __forceinline__ void wait_loads()
 
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
-// Brings tiles of KEYS keys to LDS.  The keys of a tile are 16-key groups, each
-// on one page; lane i of a wave keeps the place in the cache of the i-th group
-// to come, 64 groups at a time.  Groups on no page, or past `end`, are read
-// from page 0 and hidden later, so every read is inside the cache.
+// Brings tiles of keys to LDS.  The keys of a tile are 16-key groups, each on
+// one page; lane i of a wave keeps the place in the cache of the i-th group to
+// come, 64 groups at a time.  Groups on no page, or past `end`, are read from
+// page 0 and hidden later, so every read is inside the cache.
 //
-// WAVES waves share a tile; 16-bit caches go straight to LDS, e4m3 ones are
-// read into registers (fetch) and widened on the way to LDS (store).
-template <int DT, int CDT, int DP, int KEYS, int WAVES>
+// A tile of 64 keys is shared by four waves, a group each; a tile of 32 is one
+// wave's own.  16-bit caches go straight to LDS, e4m3 ones are read into
+// registers (fetch) and widened on the way to LDS (store).
+template <int DT, int CDT, int DP, bool SHARED>
 struct Stage {
     using L = Tiles<DP>;
     using C = typename Elem<CDT>::type;
     static constexpr int VT = Types<DT, CDT>::V;
     static constexpr bool kDirect = CDT != kE4M3;
-    static constexpr int kGroups = KEYS / 16;
-    static constexpr int kLoads = KEYS * L::kPieces / kLanes;       // 64-lane loads of a tile
-    static constexpr int kSlots = (kLoads + WAVES - 1) / WAVES;     // of them, a wave's
+    static constexpr int kGroups = SHARED ? 4 : 2;
+    static constexpr int kMine = SHARED ? 1 : 2;                    // groups a wave reads
+    static constexpr int kParts = (L::kPieces + 3) / 4;             // 64-lane loads of a group,
+    static constexpr bool kHalfPart = L::kPieces % 4 != 0;          // the last one of 32 lanes
+    static constexpr int kLoads = kMine * kParts;                   // a wave's loads of a tile
     static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of groups
-    // a load stays within one group, or reaches into the next
-    static constexpr bool kOneGroup = L::kPieces % 4 == 0;
+    static constexpr int kGroupBytes = 16 * L::kRow;
 
     const AttnParams &p;
     const int32_t *table;
@@ -278,8 +280,8 @@ struct Stage {
     int row_bytes;
     uint32_t group_lo, group_hi;               // lane's group: its byte offset in the cache
     uint64_t have;                             // groups that are on a page
-    int offset[2][kSlots];                     // lane's pieces: bytes from their group, -1 for a zero
-    u32x2 k[kDirect ? 1 : kSlots], v[kDirect ? 1 : kSlots];
+    int offset[2][kParts];                     // lane's pieces: bytes from their group, -1 for a zero
+    u32x2 k[kDirect ? 1 : kLoads], v[kDirect ? 1 : kLoads];
 
     __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
                      int stride, int end)
@@ -288,8 +290,8 @@ struct Stage {
           row_bytes(p.head_dim * int(sizeof(C)))
     {
 #pragma unroll
-        for (int n = 0; n < kSlots; ++n) {
-            const int id = (n * WAVES + wave) * kLanes + (int(threadIdx.x) & (kLanes - 1));
+        for (int n = 0; n < kParts; ++n) {
+            const int id = n * kLanes + (int(threadIdx.x) & (kLanes - 1));
             const int key = id / L::kPieces, at = id % L::kPieces;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -322,182 +324,107 @@ struct Stage {
         return uint32_t(have >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
     }
 
-    __device__ __forceinline__ const char *group_at(const void *cache, int tile, int group) const
-    {
-        const int lane = tile % kBatch * kGroups + group;
-        const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), lane));
-        const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), lane));
-        return static_cast<const char *>(cache) + (hi << 32 | lo);
-    }
-
     // Issues a tile's reads of keys or of values (to LDS address lds).
     template <bool VALUES>
     __device__ __forceinline__ void fetch(int tile, uint32_t lds)
     {
-        const void *cache = VALUES ? p.paged.v_cache : p.paged.k_cache;
+        const char *cache = static_cast<const char *>(VALUES ? p.paged.v_cache : p.paged.k_cache);
         const bool exact = p.head_dim == DP;
 #pragma unroll
-        for (int n = 0; n < kSlots; ++n) {
-            const int m = n * WAVES + wave;
-            if (kLoads % WAVES != 0 && m >= kLoads) continue;
-            const int group = m * kLanes / L::kPieces / 16;
-            const char *base = group_at(cache, tile, group);
-            const int off = offset[VALUES][n];
-            if (kOneGroup && exact) {
-                if constexpr (kDirect) load_to_lds(base, uint32_t(off), lds + m * 1024);
-                else (VALUES ? v : k)[n] = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
-                continue;
+        for (int i = 0; i < kMine; ++i) {
+            const int group = SHARED ? wave : i;
+            const int from_lane = tile % kBatch * kGroups + group;
+            const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), from_lane));
+            const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), from_lane));
+            const char *base = cache + (hi << 32 | lo);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                const uint32_t to = lds + group * kGroupBytes + n * 1024;
+                const int off = offset[VALUES][n];
+                const bool on = !kHalfPart || n + 1 < kParts || (int(threadIdx.x) & 32) == 0;
+                if constexpr (kDirect) {
+                    if (!on) continue;
+                    if (exact)
+                        load_to_lds(base, uint32_t(off), to);
+                    else
+                        load_to_lds(off < 0 ? reinterpret_cast<const char *>(&kZeroPiece) : base + off, to);
+                } else {
+                    u32x2 x = 0u;
+                    if (on && off >= 0) x = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
+                    (VALUES ? v : k)[i * kParts + n] = x;
+                }
             }
-            const char *from = base + off;
-            if constexpr (!kOneGroup) {
-                const int next = min(group + 1, kGroups - 1);
-                const int key = (m * kLanes + (int(threadIdx.x) & (kLanes - 1))) / L::kPieces;
-                const char *other = group_at(cache, tile, next) + off;
-                from = key / 16 == group ? from : other;
-            }
-            if (!exact && off < 0) from = reinterpret_cast<const char *>(&kZeroPiece);
-            if constexpr (kDirect) load_to_lds(from, lds + m * 1024);
-            else (VALUES ? v : k)[n] = *reinterpret_cast<const u32x2 *>(from);
         }
+    }
+
+    // Calls f(byte in the tile, key) for each of this lane's pieces.
+    template <typename F>
+    __device__ __forceinline__ void each_piece(F f) const
+    {
+        const int lane = int(threadIdx.x) & (kLanes - 1);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                if (kHalfPart && n + 1 == kParts && lane >= 32) continue;
+                const int id = n * kLanes + lane, group = SHARED ? wave : i;
+                f(group * kGroupBytes + id * 16, group * 16 + id / L::kPieces, i * kParts + n);
+            }
     }
 
     // e4m3: what fetch read, widened, to LDS.
     template <bool VALUES>
     __device__ __forceinline__ void store(char *lds)
     {
-        if constexpr (!kDirect) {
-#pragma unroll
-            for (int n = 0; n < kSlots; ++n) {
-                const int m = n * WAVES + wave;
-                if (kLoads % WAVES != 0 && m >= kLoads) continue;
-                const u32x2 x = (VALUES ? v : k)[n];
-                *reinterpret_cast<u32x4 *>(lds + m * 1024 + (int(threadIdx.x) & (kLanes - 1)) * 16) =
-                    widen<VALUES ? VT : DT>(x);
-            }
-        }
+        if constexpr (!kDirect)
+            each_piece([&](int at, int, int n) {
+                *reinterpret_cast<u32x4 *>(lds + at) = widen<VALUES ? VT : DT>((VALUES ? v : k)[n]);
+            });
     }
 
     // Values of places that no row sees become zeros (the tail of a page may
     // hold anything, and 0 * NaN is not 0); so do infinities and NaN that some
     // rows see and others do not, which set bad.
-    __device__ __forceinline__ void clean_values(char *lds, int tile, uint32_t there, int *bad)
+    __device__ __forceinline__ void clean_values(char *lds, int tile, uint32_t there, int *bad) const
     {
         const int key0 = first + tile * stride;
-#pragma unroll 1
-        for (int n = 0; n < kSlots; ++n) {
-            const int m = n * WAVES + wave;
-            if (m >= kLoads) continue;
-            const int id = m * kLanes + (int(threadIdx.x) & (kLanes - 1));
-            const int key = id / L::kPieces;
-            u32x4 *at = reinterpret_cast<u32x4 *>(lds + id * 16);
+        each_piece([&](int at, int key, int) {
+            u32x4 *x = reinterpret_cast<u32x4 *>(lds + at);
             if (key0 + key >= end || !((there >> (key / 16)) & 1)) {
-                *at = 0;
-            } else if (non_finite<VT>(*at)) {
-                *at = finite_only<VT>(*at);
+                *x = 0;
+            } else if (non_finite<VT>(*x)) {
+                *x = finite_only<VT>(*x);
                 *bad = 1;
             }
-        }
+        });
     }
 };
 
-// S^T of one tile for a wave's rows.  The operands are read a batch ahead of
-// the matrix instructions that use them, and the barriers keep it so: left
-// alone, the compiler puts each read right before its use, and the wave waits
-// out the latency of LDS every time.
-template <int DT, int DP, int KT>
-__device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<DP>::kSteps],
-                                       const char *keys)
-{
+// Keeps what comes before it before what comes after it.  Left alone, the
+// compiler puts each LDS read right before its use and gathers matrix
+// instructions apart from the arithmetic that could run beside them.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// The operands of S^T: key `lane % 32` of each 32, 16 dims a step.
+template <int DP>
+struct KeyReads {
     using L = Tiles<DP>;
-    constexpr int kReads = KT * L::kSteps, kBatch = 8, kBatches = (kReads + kBatch - 1) / kBatch;
-    const int lane = int(threadIdx.x) & (kLanes - 1);
-    const int col = lane & 31, piece = (lane >> 5) ^ L::key_swizzle(col);
-    const char *row = keys + col * L::kRow;
-    u32x4 a[2][kBatch];
-    const auto read = [&](int batch) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int n = batch * kBatch + i;
-            if (n < kReads)
-                a[batch & 1][i] = *reinterpret_cast<const u32x4 *>(
-                    row + n / L::kSteps * 32 * L::kRow + ((piece ^ (2 * (n % L::kSteps))) << 4));
-        }
-    };
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) s[kt] = 0.0f;
-    read(0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int batch = 0; batch < kBatches; ++batch) {
-        if (batch + 1 < kBatches) read(batch + 1);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int n = batch * kBatch + i;
-            if (n < kReads) s[n / L::kSteps] = mfma<DT>(a[batch & 1][i], q[n % L::kSteps], s[n / L::kSteps]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
+    const char *row;
+    int piece;
 
-// Hides what a row does not see: key j of the tile is seen in [lo, hi)
-// (relative to the tile) if its 16-key group is there.
-template <int KT>
-__device__ __forceinline__ void hide(f32x16 (&s)[KT], int lo, int hi, uint32_t there)
-{
-    // register i holds key kt * 32 + 8 (i / 4) + i % 4 + 4 half; the half goes
-    // to the limits, so that the rest is a constant
-    const int half = (int(threadIdx.x) & (kLanes - 1)) >> 5;
-    lo -= 4 * half;
-    hi -= 4 * half;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int key = kt * 32 + 8 * (i / 4) + i % 4;
-            const bool seen = key >= lo && key < hi && ((there >> (kt * 2 + i / 8)) & 1);
-            s[kt][i] = seen ? s[kt][i] : -INFINITY;
-        }
-}
-
-// Scores to weights: the running maximum and sum, O rescaled where the
-// maximum moved, the weights in w as operands of the second product.
-template <int VT, int DP, int KT>
-__device__ __forceinline__ void weights(Rows<DP> &r, f32x16 (&s)[KT], u32x4 (&w)[2 * KT], float c)
-{
-    float top = s[0][0];
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kt][i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
-    // The reference maximum moves only when a row's weights would pass 2^8:
-    // any reference within that of the true maximum gives the same softmax,
-    // and most tiles then leave O as it is.
-    if (__any(top * c > r.top * c + 8.0f || (r.top == -INFINITY && top > -INFINITY))) {
-        const float now = fmaxf(r.top, top);
-        const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
-        r.top = now;
-        r.sum *= keep;
-#pragma unroll
-        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] *= keep;
+    __device__ explicit KeyReads(const char *keys)
+    {
+        const int lane = int(threadIdx.x) & (kLanes - 1), col = lane & 31;
+        piece = (lane >> 5) ^ L::key_swizzle(col);
+        row = keys + col * L::kRow;
     }
-    const float base = r.top == -INFINITY ? 0.0f : r.top * c;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[kt][i] = __builtin_amdgcn_exp2f(fmaf(s[kt][i], c, -base));
-            r.sum += s[kt][i];
-        }
-        const f32x8 a = __builtin_shufflevector(s[kt], s[kt], 0, 1, 2, 3, 4, 5, 6, 7);
-        const f32x8 b = __builtin_shufflevector(s[kt], s[kt], 8, 9, 10, 11, 12, 13, 14, 15);
-        using F = typename Frag<VT>::type;
-        w[2 * kt] = __builtin_bit_cast(u32x4, __builtin_convertvector(a, F));
-        w[2 * kt + 1] = __builtin_bit_cast(u32x4, __builtin_convertvector(b, F));
+    __device__ __forceinline__ u32x4 operator()(int block, int step) const
+    {
+        return *reinterpret_cast<const u32x4 *>(row + block * 32 * L::kRow + ((piece ^ (2 * step)) << 4));
     }
-}
+};
 
-// Operands of O^T for 16 keys: V^T, 32 dims each.
+// The operands of O^T for 16 keys: V^T, 32 dims each.
 template <int DP> struct Values { u32x4 a[Tiles<DP>::kDims]; };
 
 template <int DP>
@@ -523,6 +450,117 @@ __device__ __forceinline__ Values<DP> read_values(const char *values, int u)
     return x;
 }
 
+// Hides what a row does not see: key j of the tile is seen in [lo, hi)
+// (relative to the tile) if its 16-key group is there.
+template <int KT>
+__device__ __forceinline__ void hide(f32x16 (&s)[KT], int lo, int hi, uint32_t there)
+{
+    // register i holds key kt * 32 + 8 (i / 4) + i % 4 + 4 half; the half goes
+    // to the limits, so that the rest is a constant
+    const int half = (int(threadIdx.x) & (kLanes - 1)) >> 5;
+    lo -= 4 * half;
+    hi -= 4 * half;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int key = kt * 32 + 8 * (i / 4) + i % 4;
+            const bool seen = key >= lo && key < hi && ((there >> (kt * 2 + i / 8)) & 1);
+            s[kt][i] = seen ? s[kt][i] : -INFINITY;
+        }
+}
+
+// The larger of a column's two halves.
+__device__ __forceinline__ float both_halves(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_elementwise_maximum(__builtin_bit_cast(float, uint32_t(r[0])),
+                                         __builtin_bit_cast(float, uint32_t(r[1])));
+}
+
+// Takes a tile's largest score into the running maximum.  The reference moves
+// only when a row's weights would pass 2^8: any reference within that of the
+// true maximum gives the same softmax, and most tiles then leave O as it is.
+// Returns the reference times c (0 while no key has been seen).
+template <int DP>
+__device__ __forceinline__ float move_top(Rows<DP> &r, float top, float c)
+{
+    if (__any(top * c > r.top * c + 8.0f || (r.top == -INFINITY && top > -INFINITY))) {
+        const float now = fmaxf(r.top, top);
+        const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
+        r.top = now;
+        r.sum *= keep;
+#pragma unroll
+        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] *= keep;
+    }
+    return r.top == -INFINITY ? 0.0f : r.top * c;
+}
+
+// Scores to weights, added to sum and rounded to VT.
+template <int VT, int KT>
+__device__ __forceinline__ void exponentials(f32x16 (&s)[KT], u32x4 (&w)[2 * KT], float &sum, float c,
+                                             float base)
+{
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[kt][i] = __builtin_amdgcn_exp2f(fmaf(s[kt][i], c, -base));
+            sum += s[kt][i];
+        }
+        const f32x8 a = __builtin_shufflevector(s[kt], s[kt], 0, 1, 2, 3, 4, 5, 6, 7);
+        const f32x8 b = __builtin_shufflevector(s[kt], s[kt], 8, 9, 10, 11, 12, 13, 14, 15);
+        using F = typename Frag<VT>::type;
+        w[2 * kt] = __builtin_bit_cast(u32x4, __builtin_convertvector(a, F));
+        w[2 * kt + 1] = __builtin_bit_cast(u32x4, __builtin_convertvector(b, F));
+    }
+}
+
+// S^T of one tile, its operands read a batch ahead.
+template <int DT, int DP, int KT>
+__device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<DP>::kSteps],
+                                       const char *keys)
+{
+    using L = Tiles<DP>;
+    constexpr int kReads = KT * L::kSteps, kBatch = 8, kBatches = (kReads + kBatch - 1) / kBatch;
+    const KeyReads<DP> read(keys);
+    u32x4 a[2][kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch && i < kReads; ++i) a[0][i] = read(i % KT, i / KT);
+    in_order();
+#pragma unroll
+    for (int batch = 0; batch < kBatches; ++batch) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int n = (batch + 1) * kBatch + i;
+            if (n < kReads) a[(batch + 1) & 1][i] = read(n % KT, n / KT);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int n = batch * kBatch + i;
+            if (n >= kReads) continue;
+            f32x16 &o = s[n % KT];
+            o = mfma<DT>(a[batch & 1][i], q[n / KT], n < KT ? f32x16(0.0f) : o);
+        }
+        in_order();
+    }
+}
+
+// The largest of a lane's scores; NaN if one is (its row's sum is then NaN
+// whatever the reference).  Three operands an instruction, and unlike fmaxf no
+// extra one to quiet each score.
+template <int KT>
+__device__ __forceinline__ float largest(const f32x16 (&s)[KT])
+{
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < KT * 16; n += 2)
+        top[n / 2 % 2] = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(s[n / 16][n % 16], s[n / 16][n % 16 + 1]), top[n / 2 % 2]);
+    return __builtin_elementwise_maximum(top[0], top[1]);
+}
+
 // O^T += V^T P^T; ready: the operands of the tile's first 16 keys.
 template <int VT, int DP, int KT>
 __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT], const char *values,
@@ -530,12 +568,12 @@ __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT]
 {
 #pragma unroll
     for (int u = 0; u < KT * 2; ++u) {
-        Values<DP> next;
-        if (u + 1 < KT * 2) next = read_values<DP>(values, u + 1);
+        Values<DP> more;
+        if (u + 1 < KT * 2) more = read_values<DP>(values, u + 1);
 #pragma unroll
         for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] = mfma<VT>(ready.a[dt], w[u], r.o[dt]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (u + 1 < KT * 2) ready = next;
+        in_order();
+        if (u + 1 < KT * 2) ready = more;
     }
 }
 
@@ -628,8 +666,8 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
         for (int st = 0; st < L::kSteps; ++st) asm volatile("" : "+v"(q[st]));
     }
     // limits of all of the wave's rows (they grow with the row)
-    const int wave_lo = __shfl(lo, 0), wave_hi = __shfl(hi, 31);
-    const int all_lo = __shfl(lo, 31), all_hi = __shfl(hi, 0);
+    const int wave_lo = __builtin_amdgcn_readlane(lo, 0), wave_hi = __builtin_amdgcn_readlane(hi, 31);
+    const int all_lo = __builtin_amdgcn_readlane(lo, 31), all_hi = __builtin_amdgcn_readlane(hi, 0);
     const float c = p.scale * g.k_scale * kLog2e;
 
     if (threadIdx.x == 0) bad = 0;
@@ -644,7 +682,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     if (!by_keys) {
         // two buffers of 64 keys: a tile's reads run while the one before it
         // is worked on
-        using S = Stage<DT, CDT, DP, 64, kWavesPerBlock>;
+        using S = Stage<DT, CDT, DP, true>;
         S st(p, w, kv_head, wave, from, 64, to);
         constexpr int kHalf = 64 * L::kRow;
         // keys that every row of the block sees; elsewhere values are looked at
@@ -658,7 +696,6 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             st.template fetch<false>(0, at);
             st.template fetch<true>(0, at + kHalf);
         }
-        uint32_t there = n_tiles > 0 ? st.groups_there(0) : 0;
         for (int tile = 0; tile < n_tiles; ++tile) {
             char *keys = lds + (tile & 1) * 2 * kHalf, *values = keys + kHalf;
             const int key0 = from + tile * 64;
@@ -669,34 +706,34 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
                 st.template store<true>(values);
             }
             __syncthreads();
-            const uint32_t now = there;
+            const uint32_t there = st.groups_there(tile);
             if (tile + 1 < n_tiles) {
                 if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
-                there = st.groups_there(tile + 1);
                 const uint32_t next = at + ((tile + 1) & 1) * 2 * kHalf;
                 st.template fetch<false>(tile + 1, next);
                 st.template fetch<true>(tile + 1, next + kHalf);
             }
-            if (key0 < blo || key0 + 64 > bhi || now != 15) {
-                st.clean_values(values, tile, now, &bad);
+            if (key0 < blo || key0 + 64 > bhi || there != 15) {
+                st.clean_values(values, tile, there, &bad);
                 __syncthreads();
             }
             if (key0 < wave_hi && key0 + 64 > wave_lo) {
                 f32x16 s[2];
                 u32x4 x[4];
                 scores<DT, DP, 2>(s, q, keys);
-                if (key0 < all_lo || key0 + 64 > min(all_hi, to) || now != 15)
-                    hide<2>(s, lo - key0, min(hi, to) - key0, now);
+                if (key0 < all_lo || key0 + 64 > min(all_hi, to) || there != 15)
+                    hide<2>(s, lo - key0, min(hi, to) - key0, there);
                 const Values<DP> ready = read_values<DP>(values, 0);
-                __builtin_amdgcn_sched_barrier(0);
-                weights<VT, DP, 2>(r, s, x, c);
+                in_order();
+                const float base = move_top<DP>(r, both_halves(largest<2>(s)), c);
+                exponentials<VT, 2>(s, x, r.sum, c, base);
                 add_values<VT, DP, 2>(r, x, values, ready);
             }
         }
     } else {
         // a buffer of 32 keys for each wave: the next keys are read once the
         // scores are done with these, the next values once O is
-        using S = Stage<DT, CDT, DP, 32, 1>;
+        using S = Stage<DT, CDT, DP, false>;
         constexpr int kStep = 32 * kWavesPerBlock;
         constexpr int kHalf = 32 * L::kRow;
         const int first_key = from + wave * 32;
@@ -716,7 +753,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             f32x16 s[1];
             u32x4 x[2];
             if constexpr (S::kDirect) {
-                wait_loads<S::kSlots>();                 // the values may be on their way
+                wait_loads<S::kLoads>();                 // the values may be on their way
             } else {
                 st.template store<false>(keys);
                 st.template store<true>(values);
@@ -730,9 +767,10 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             }
             const bool whole = key0 >= all_lo && key0 + 32 <= min(all_hi, to) && there == 3;
             if (!whole) hide<1>(s, lo - key0, min(hi, to) - key0, there);
-            weights<VT, DP, 1>(r, s, x, c);
+            const float base = move_top<DP>(r, both_halves(largest<1>(s)), c);
+            exponentials<VT, 1>(s, x, r.sum, c, base);
             if constexpr (S::kDirect) {
-                if (more) wait_loads<S::kSlots>();
+                if (more) wait_loads<S::kLoads>();
                 else wait_loads<0>();
             }
             if (!whole) st.clean_values(values, tile, there, &bad);

@@ -254,8 +254,8 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 // Brings tiles of keys to LDS.  The keys of a tile are 16-key groups, each on
 // one page; lane i of a wave keeps the place in the cache of the i-th group to
-// come, 64 groups at a time.  Groups on no page, or past `end`, are read from
-// page 0 and hidden later, so every read is inside the cache.
+// come, 64 groups at a time.  Groups on no page, or outside [begin, end), are
+// read from page 0 and hidden later, so every read is inside the cache.
 //
 // A tile of 64 keys is shared by four waves, a group each; a tile of 32 is one
 // wave's own.  16-bit caches go straight to LDS, e4m3 ones are read into
@@ -276,7 +276,8 @@ struct Stage {
 
     const AttnParams &p;
     const int32_t *table;
-    int kv_head, wave, end, first, stride;     // tile t holds keys first + t * stride ...
+    int kv_head, wave, begin, end;             // keys [begin, end) are wanted
+    int first, stride;                         // tile t holds keys first + t * stride ...
     int row_bytes;
     uint32_t group_lo, group_hi;               // lane's group: its byte offset in the cache
     uint64_t have;                             // groups that are on a page
@@ -284,9 +285,9 @@ struct Stage {
     u32x2 k[kDirect ? 1 : kLoads], v[kDirect ? 1 : kLoads];
 
     __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
-                     int stride, int end)
+                     int stride, int begin, int end)
         : p(p), table(p.paged.block_table + int64_t(w.seq) * p.paged.max_pages), kv_head(kv_head),
-          wave(wave), end(end), first(first), stride(stride),
+          wave(wave), begin(begin), end(end), first(first), stride(stride),
           row_bytes(p.head_dim * int(sizeof(C)))
     {
 #pragma unroll
@@ -308,7 +309,7 @@ struct Stage {
         const int lane = int(threadIdx.x) & (kLanes - 1);
         const int64_t key = first + int64_t(tile + lane / kGroups) * stride + lane % kGroups * 16;
         int page = -1;
-        if (key < end) page = table[key >> g.page_shift];
+        if (key >= begin && key < end) page = table[key >> g.page_shift];
         if (page >= g.n_pages) page = -1;
         have = __ballot(page >= 0);
         const int64_t row = ((int64_t(max(page, 0)) * p.n_k_heads + kv_head) << g.page_shift) +
@@ -405,7 +406,7 @@ struct Stage {
 // instructions apart from the arithmetic that could run beside them.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// The operands of S^T: key `lane % 32` of each 32, 16 dims a step.
+// The operands of S^T: key lane % 32 of 32, 16 dims a step.
 template <int DP>
 struct KeyReads {
     using L = Tiles<DP>;
@@ -418,56 +419,69 @@ struct KeyReads {
         piece = (lane >> 5) ^ L::key_swizzle(col);
         row = keys + col * L::kRow;
     }
-    __device__ __forceinline__ u32x4 operator()(int block, int step) const
+    __device__ __forceinline__ u32x4 operator()(int step) const
     {
-        return *reinterpret_cast<const u32x4 *>(row + block * 32 * L::kRow + ((piece ^ (2 * step)) << 4));
+        return *reinterpret_cast<const u32x4 *>(row + ((piece ^ (2 * step)) << 4));
     }
 };
 
-// The operands of O^T for 16 keys: V^T, 32 dims each.
-template <int DP> struct Values { u32x4 a[Tiles<DP>::kDims]; };
-
+// The operands of O^T, V^T: 32 dims of 16 keys a read (two of them).
 template <int DP>
-__device__ __forceinline__ Values<DP> read_values(const char *values, int u)
-{
+struct ValueReads {
     using L = Tiles<DP>;
-    using Lds = __attribute__((address_space(3))) i16x4;
-    const int lane = int(threadIdx.x) & (kLanes - 1);
-    // lane i of 16 names key i / 4, four dims from 4 (i % 4), and gets dim i, keys 0-3
-    const int key = 4 * (lane >> 5) + (lane & 15) / 4;
-    const int in_row = ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-    const int swizzle = L::value_swizzle(key) >> 2;
-    const char *from = values + key * L::kRow + in_row;
-    Values<DP> x;
-#pragma unroll
-    for (int dt = 0; dt < L::kDims; ++dt) {
+    const char *from;
+    int swizzle;
+
+    __device__ explicit ValueReads(const char *values)
+    {
+        // lane i of 16 names key i / 4, four dims from 4 (i % 4), and gets dim i, keys 0-3
+        const int lane = int(threadIdx.x) & (kLanes - 1);
+        const int key = 4 * (lane >> 5) + (lane & 15) / 4;
+        from = values + key * L::kRow + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+        swizzle = L::value_swizzle(key) >> 2;
+    }
+    __device__ __forceinline__ u32x4 operator()(int u, int dt) const       // keys 16 u ..., dims 32 dt ...
+    {
+        using Lds = __attribute__((address_space(3))) i16x4;
         const char *at = from + u * 16 * L::kRow + ((dt ^ swizzle) << 6);
         const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)at);
         const i16x4 z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(at + 8 * L::kRow));
         const u32x2 yy = __builtin_bit_cast(u32x2, y), zz = __builtin_bit_cast(u32x2, z);
-        x.a[dt] = u32x4{yy.x, yy.y, zz.x, zz.y};
+        return u32x4{yy.x, yy.y, zz.x, zz.y};
     }
-    return x;
+};
+
+// The first operands of a tile, read before they are needed.
+template <int DP> struct Ready {
+    static constexpr int kN = Tiles<DP>::kDims < 4 ? Tiles<DP>::kDims : 4;
+    u32x4 a[kN];
+};
+
+template <int DP>
+__device__ __forceinline__ Ready<DP> read_ahead(const char *values)
+{
+    const ValueReads<DP> read(values);
+    Ready<DP> r;
+#pragma unroll
+    for (int n = 0; n < Ready<DP>::kN; ++n) r.a[n] = read(0, n);
+    return r;
 }
 
-// Hides what a row does not see: key j of the tile is seen in [lo, hi)
-// (relative to the tile) if its 16-key group is there.
-template <int KT>
-__device__ __forceinline__ void hide(f32x16 (&s)[KT], int lo, int hi, uint32_t there)
+// Hides what a row does not see: key j of the 32 is seen in [lo, hi) (relative
+// to the first) if its 16-key group is there.
+__device__ __forceinline__ void hide(f32x16 &s, int lo, int hi, uint32_t there)
 {
-    // register i holds key kt * 32 + 8 (i / 4) + i % 4 + 4 half; the half goes
-    // to the limits, so that the rest is a constant
+    // register i holds key 8 (i / 4) + i % 4 + 4 half; the half goes to the
+    // limits, so that the rest is a constant
     const int half = (int(threadIdx.x) & (kLanes - 1)) >> 5;
     lo -= 4 * half;
     hi -= 4 * half;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int key = kt * 32 + 8 * (i / 4) + i % 4;
-            const bool seen = key >= lo && key < hi && ((there >> (kt * 2 + i / 8)) & 1);
-            s[kt][i] = seen ? s[kt][i] : -INFINITY;
-        }
+    for (int i = 0; i < 16; ++i) {
+        const int key = 8 * (i / 4) + i % 4;
+        const bool seen = key >= lo && key < hi && ((there >> (i / 8)) & 1);
+        s[i] = seen ? s[i] : -INFINITY;
+    }
 }
 
 // The larger of a column's two halves.
@@ -492,88 +506,93 @@ __device__ __forceinline__ float move_top(Rows<DP> &r, float top, float c)
         r.top = now;
         r.sum *= keep;
 #pragma unroll
-        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] *= keep;
+        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) {
+            r.o[dt] *= keep;
+            in_order();
+        }
     }
     return r.top == -INFINITY ? 0.0f : r.top * c;
 }
 
-// Scores to weights, added to sum and rounded to VT.
-template <int VT, int KT>
-__device__ __forceinline__ void exponentials(f32x16 (&s)[KT], u32x4 (&w)[2 * KT], float &sum, float c,
-                                             float base)
+// Scores [from, to) of 32 keys to weights, added to sum; pairs are rounded to
+// VT once both are there.
+template <int VT>
+__device__ __forceinline__ void exponentials(f32x16 &s, u32x4 (&w)[2], float &sum, float c, float base,
+                                             int from, int to)
 {
+    typedef typename Elem<VT>::type V2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[kt][i] = __builtin_amdgcn_exp2f(fmaf(s[kt][i], c, -base));
-            sum += s[kt][i];
+    for (int n = from; n < to; ++n) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[n], c, -base));
+        s[n] = x;
+        sum += x;
+        if (n % 2) {
+            const f32x2 pair = {s[n - 1], x};
+            w[n / 8][n / 2 % 4] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, V2));
         }
-        const f32x8 a = __builtin_shufflevector(s[kt], s[kt], 0, 1, 2, 3, 4, 5, 6, 7);
-        const f32x8 b = __builtin_shufflevector(s[kt], s[kt], 8, 9, 10, 11, 12, 13, 14, 15);
-        using F = typename Frag<VT>::type;
-        w[2 * kt] = __builtin_bit_cast(u32x4, __builtin_convertvector(a, F));
-        w[2 * kt + 1] = __builtin_bit_cast(u32x4, __builtin_convertvector(b, F));
     }
 }
 
-// S^T of one tile, its operands read a batch ahead.
-template <int DT, int DP, int KT>
-__device__ __forceinline__ void scores(f32x16 (&s)[KT], const u32x4 (&q)[Tiles<DP>::kSteps],
-                                       const char *keys)
+// S^T of 32 keys.  The matrix instructions run beside the exponentials of the
+// 32 keys before (BESIDE): a wave issues one and goes on, and 16 scores take
+// about as long as the head's instructions do.
+template <int DT, int VT, int DP, bool BESIDE>
+__device__ __forceinline__ void scores(f32x16 &out, const u32x4 (&q)[Tiles<DP>::kSteps],
+                                       const char *keys, f32x16 &s, u32x4 (&w)[2], float &sum, float c,
+                                       float base)
 {
-    using L = Tiles<DP>;
-    constexpr int kReads = KT * L::kSteps, kBatch = 8, kBatches = (kReads + kBatch - 1) / kBatch;
+    constexpr int kN = Tiles<DP>::kSteps, kAhead = kN < 4 ? kN : 4;
     const KeyReads<DP> read(keys);
-    u32x4 a[2][kBatch];
+    u32x4 a[kAhead];
 #pragma unroll
-    for (int i = 0; i < kBatch && i < kReads; ++i) a[0][i] = read(i % KT, i / KT);
+    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
     in_order();
+    f32x16 o = 0.0f;
 #pragma unroll
-    for (int batch = 0; batch < kBatches; ++batch) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int n = (batch + 1) * kBatch + i;
-            if (n < kReads) a[(batch + 1) & 1][i] = read(n % KT, n / KT);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int n = batch * kBatch + i;
-            if (n >= kReads) continue;
-            f32x16 &o = s[n % KT];
-            o = mfma<DT>(a[batch & 1][i], q[n / KT], n < KT ? f32x16(0.0f) : o);
-        }
+    for (int n = 0; n < kN; ++n) {
+        o = mfma<DT>(a[n % kAhead], q[n], o);
+        if (n + kAhead < kN) a[n % kAhead] = read(n + kAhead);
+        if constexpr (BESIDE) exponentials<VT>(s, w, sum, c, base, n * 16 / kN, (n + 1) * 16 / kN);
         in_order();
     }
+    out = o;
 }
 
 // The largest of a lane's scores; NaN if one is (its row's sum is then NaN
 // whatever the reference).  Three operands an instruction, and unlike fmaxf no
 // extra one to quiet each score.
-template <int KT>
-__device__ __forceinline__ float largest(const f32x16 (&s)[KT])
+__device__ __forceinline__ float larger(float top, const f32x16 &s, int n)
 {
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < KT * 16; n += 2)
-        top[n / 2 % 2] = __builtin_elementwise_maximum(
-            __builtin_elementwise_maximum(s[n / 16][n % 16], s[n / 16][n % 16 + 1]), top[n / 2 % 2]);
-    return __builtin_elementwise_maximum(top[0], top[1]);
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(s[n], s[n + 1]), top);
 }
 
-// O^T += V^T P^T; ready: the operands of the tile's first 16 keys.
-template <int VT, int DP, int KT>
-__device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2 * KT], const char *values,
-                                           Values<DP> ready)
+__device__ __forceinline__ float largest(const f32x16 &s)
 {
+    float top = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < KT * 2; ++u) {
-        Values<DP> more;
-        if (u + 1 < KT * 2) more = read_values<DP>(values, u + 1);
+    for (int n = 0; n < 16; n += 2) top = larger(top, s, n);
+    return top;
+}
+
+// O^T += V^T P^T for 32 keys; the largest of the next scores is found beside
+// it (BESIDE).
+template <int VT, int DP, bool BESIDE>
+__device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2], const char *values,
+                                           Ready<DP> ready, const f32x16 &next, float &top)
+{
+    constexpr int kDims = Tiles<DP>::kDims, kN = 2 * kDims, kAhead = Ready<DP>::kN;
+    const ValueReads<DP> read(values);
+    if constexpr (BESIDE) top = -INFINITY;
 #pragma unroll
-        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) r.o[dt] = mfma<VT>(ready.a[dt], w[u], r.o[dt]);
+    for (int n = 0; n < kN; ++n) {
+        r.o[n % kDims] = mfma<VT>(ready.a[n % kAhead], w[n / kDims], r.o[n % kDims]);
+        const int m = n + kAhead;
+        if (m < kN) ready.a[n % kAhead] = read(m / kDims, m % kDims);
+        if constexpr (BESIDE) {
+#pragma unroll
+            for (int i = n * 8 / kN; i < (n + 1) * 8 / kN; ++i) top = larger(top, next, 2 * i);
+        }
         in_order();
-        if (u + 1 < KT * 2) ready = more;
     }
 }
 
@@ -680,54 +699,85 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
 
     const uint32_t at = lds_address(lds);
     if (!by_keys) {
-        // two buffers of 64 keys: a tile's reads run while the one before it
-        // is worked on
+        // Turns of 64 keys in two halves.  While a wave turns the scores of 32
+        // keys into weights, the matrix cores compute the scores of the next
+        // 32; while they add its values, it finds the next maximum.  Keys are
+        // therefore wanted half a turn before their values: the key tiles in
+        // LDS lie 32 keys further on.  Two buffers each; a turn's reads run
+        // for the whole turn before it.
         using S = Stage<DT, CDT, DP, true>;
-        S st(p, w, kv_head, wave, from, 64, to);
-        constexpr int kHalf = 64 * L::kRow;
+        S sk(p, w, kv_head, wave, from + 32, 64, from, to), sv(p, w, kv_head, wave, from, 64, from, to);
+        constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf;
         // keys that every row of the block sees; elsewhere values are looked at
         int blo, bhi, unused;
         row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
         row_limits(p, w, w.row0, group, unused, bhi);
         bhi = min(bhi, to);
-        const int n_tiles = (to - from + 63) / 64;
-        if (n_tiles > 0) {
-            st.find_pages(0);
-            st.template fetch<false>(0, at);
-            st.template fetch<true>(0, at + kHalf);
-        }
-        for (int tile = 0; tile < n_tiles; ++tile) {
-            char *keys = lds + (tile & 1) * 2 * kHalf, *values = keys + kHalf;
-            const int key0 = from + tile * 64;
+        const int n_turns = (to - from + 63) / 64;
+        // turns [mine, done) have keys that a row of this wave sees
+        const int mine = max(wave_lo - from, 0) / 64, done = (min(wave_hi, to) - from + 63) >> 6;
+        const int plain_lo = all_lo, plain_hi = min(all_hi, to) - 32;
+        uint32_t now_there = 0, next_there = 0;        // groups of this turn, of the next
+        const auto pages_of = [&](int t) {
+            if (t % S::kBatch == 0) sv.find_pages(t);
+            return sv.groups_there(t);
+        };
+        const auto hidden = [&](int key0, uint32_t there, f32x16 &y) {
+            if (key0 >= plain_lo && key0 <= plain_hi && there == 3) return;
+            hide(y, lo - key0, min(hi, to) - key0, there);
+        };
+        // key tile t: keys 32-63 of turn t, then 0-31 of turn t + 1
+        const auto read_keys = [&](int t) {
+            if ((t + 1) % S::kBatch == 0) sk.find_pages(t + 1);
+            sk.template fetch<false>(t + 1, at + ((t + 1) & 1) * kTile);
+        };
+        sk.first -= 64;                                // its tile 0 is key tile -1
+        f32x16 a = 0.0f, b = 0.0f;                     // scores of a turn's halves
+        u32x4 x[2];
+        float top = -INFINITY, none = 0.0f;
+        if (n_turns > 0) read_keys(-1);
+        for (int t = -1; t < n_turns; ++t) {
+            char *keys = lds + ((t + 1) & 1) * kTile, *values = lds + (2 + (t & 1)) * kTile;
             if constexpr (S::kDirect) {
                 wait_loads<0>();
             } else {
-                st.template store<false>(keys);
-                st.template store<true>(values);
+                sk.template store<false>(keys);
+                if (t >= 0) sv.template store<true>(values);
             }
             __syncthreads();
-            const uint32_t there = st.groups_there(tile);
-            if (tile + 1 < n_tiles) {
-                if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
-                const uint32_t next = at + ((tile + 1) & 1) * 2 * kHalf;
-                st.template fetch<false>(tile + 1, next);
-                st.template fetch<true>(tile + 1, next + kHalf);
+            // every wave is done with the last turn's buffers
+            now_there = next_there;
+            if (t + 1 < n_turns) {
+                next_there = pages_of(t + 1);
+                sv.template fetch<true>(t + 1, at + (2 + ((t + 1) & 1)) * kTile);
+                read_keys(t + 1);
             }
-            if (key0 < blo || key0 + 64 > bhi || there != 15) {
-                st.clean_values(values, tile, there, &bad);
+            const int key0 = from + t * 64;
+            if (t >= 0 && (key0 < blo || key0 + 64 > bhi || now_there != 15)) {
+                sv.clean_values(values, t, now_there, &bad);
                 __syncthreads();
             }
-            if (key0 < wave_hi && key0 + 64 > wave_lo) {
-                f32x16 s[2];
-                u32x4 x[4];
-                scores<DT, DP, 2>(s, q, keys);
-                if (key0 < all_lo || key0 + 64 > min(all_hi, to) || there != 15)
-                    hide<2>(s, lo - key0, min(hi, to) - key0, there);
-                const Values<DP> ready = read_values<DP>(values, 0);
+            const bool more = t + 1 >= mine && t + 1 < done;
+            if (t >= mine && t < done && t >= 0) {
+                float base = move_top<DP>(r, both_halves(top), c);
+                scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, base);
+                Ready<DP> ready = read_ahead<DP>(values);
+                hidden(key0 + 32, now_there >> 2, b);
                 in_order();
-                const float base = move_top<DP>(r, both_halves(largest<2>(s)), c);
-                exponentials<VT, 2>(s, x, r.sum, c, base);
-                add_values<VT, DP, 2>(r, x, values, ready);
+                add_values<VT, DP, true>(r, x, values, ready, b, top);
+                base = move_top<DP>(r, both_halves(top), c);
+                // the last turn has no next scores: its maximum is then of old
+                // ones, and nobody asks for it
+                if (more) scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, base);
+                else exponentials<VT>(b, x, r.sum, c, base, 0, 16);
+                ready = read_ahead<DP>(values + kHalf);
+                if (more) hidden(key0 + 64, next_there & 3, a);
+                in_order();
+                add_values<VT, DP, true>(r, x, values + kHalf, ready, a, top);
+            } else if (more) {
+                scores<DT, VT, DP, false>(a, q, keys + kHalf, b, x, none, c, 0.0f);
+                hidden(key0 + 64, next_there & 3, a);
+                top = largest(a);
             }
         }
     } else {
@@ -737,7 +787,7 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
         constexpr int kStep = 32 * kWavesPerBlock;
         constexpr int kHalf = 32 * L::kRow;
         const int first_key = from + wave * 32;
-        S st(p, w, kv_head, 0, first_key, kStep, to);
+        S st(p, w, kv_head, 0, first_key, kStep, from, to);
         char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
         const uint32_t keys_at = at + wave * 2 * kHalf, values_at = keys_at + kHalf;
         const int n_tiles = to > first_key ? (to - first_key + kStep - 1) / kStep : 0;
@@ -750,15 +800,16 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
             const int key0 = first_key + tile * kStep;
             const bool more = tile + 1 < n_tiles;
             const uint32_t there = st.groups_there(tile);
-            f32x16 s[1];
+            f32x16 s;
             u32x4 x[2];
+            float unused;
             if constexpr (S::kDirect) {
                 wait_loads<S::kLoads>();                 // the values may be on their way
             } else {
                 st.template store<false>(keys);
                 st.template store<true>(values);
             }
-            scores<DT, DP, 1>(s, q, keys);
+            scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f);
             if (more) {
                 if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
                 wait_lds();
@@ -766,15 +817,15 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
                 if constexpr (!S::kDirect) st.template fetch<true>(tile + 1, values_at);
             }
             const bool whole = key0 >= all_lo && key0 + 32 <= min(all_hi, to) && there == 3;
-            if (!whole) hide<1>(s, lo - key0, min(hi, to) - key0, there);
-            const float base = move_top<DP>(r, both_halves(largest<1>(s)), c);
-            exponentials<VT, 1>(s, x, r.sum, c, base);
+            if (!whole) hide(s, lo - key0, min(hi, to) - key0, there);
+            const float base = move_top<DP>(r, both_halves(largest(s)), c);
+            exponentials<VT>(s, x, r.sum, c, base, 0, 16);
             if constexpr (S::kDirect) {
                 if (more) wait_loads<S::kLoads>();
                 else wait_loads<0>();
             }
             if (!whole) st.clean_values(values, tile, there, &bad);
-            add_values<VT, DP, 1>(r, x, values, read_values<DP>(values, 0));
+            add_values<VT, DP, false>(r, x, values, read_ahead<DP>(values), s, unused);
             if constexpr (S::kDirect) {
                 wait_lds();
                 if (more) st.template fetch<true>(tile + 1, values_at);

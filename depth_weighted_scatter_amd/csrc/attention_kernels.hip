@@ -2,12 +2,13 @@
 //
 // The query heads that share a key head are rows of one product: the rows of
 // a (sequence, key head) are r = token * G + g, G = n_q_heads / n_k_heads.  A
-// block takes up to 128 consecutive rows and a range of keys, in one of two
-// ways: with more than 32 rows each of its four waves owns 32 rows and all
-// walk the keys together ("rows"); with 32 or fewer every wave takes the same
-// rows and every fourth tile of 32 keys ("keys"), and the waves join at the
-// end.  Ranges of keys are cut over blocks when rows alone do not fill the
-// chip, and attend_join adds their parts.
+// block of eight waves takes a tile of consecutive rows and a range of keys.
+// A wave owns 32 rows; with 256 rows in a tile the waves walk the keys
+// together, with 128 four of them take every other 64 keys, and with 32 or
+// fewer each takes every eighth 32 keys; waves with the same rows join at the
+// end, in LDS.  Ranges of keys are cut over blocks when tiles alone do not
+// fill the chip, and attend_join adds their parts.  (Heads over 128 wide fill
+// a wave's registers: their blocks have four waves and 128 rows.)
 //
 // Both products run on 32 x 32 x 16 matrix instructions, transposed:
 //     S^T [keys x rows] = K Q^T,      O^T [dim x rows] += V^T P^T,
@@ -26,12 +27,9 @@
 namespace bevpool {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kWavesPerBlock = kBlock / kLanes;
 constexpr int kRowsPerWave = 32;
-constexpr int kRowsPerBlock = kWavesPerBlock * kRowsPerWave;
-constexpr int kUnit = 128;            // keys: ranges of a split are multiples of this
-constexpr int kMinUnits = 2;          // and at least this many
+constexpr int kUnit = 256;            // keys: ranges of a split are multiples of this
+constexpr int kMinUnits = 1;          // and at least this many
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -71,9 +69,10 @@ template <int DP> struct Tiles {
     static constexpr int kRow = DP * 2;
     static constexpr int kRound = kPieces & -kPieces;      // largest power of 2 in kPieces
     static constexpr int kSpread = kRound < 16 ? kRound : 16;
-    static constexpr int kBuffers = 8 * 32 * kRow;         // keys and values of 128 keys
+    static constexpr int kWaves = DP > 128 ? 4 : 8;        // of a block
+    static constexpr int kBuffers = kWaves * 2 * 32 * kRow;     // keys and values of 32 for each
     static constexpr int kSumRow = DP + 4;                 // floats of a row on the way out
-    static constexpr int kSums = kWavesPerBlock * 32 * kSumRow * 4;
+    static constexpr int kSums = kWaves * 32 * kSumRow * 4;
     // room past the last row: the last 32-dim piece of a 16-dim remainder reads it
     static constexpr int kLds = (kBuffers > kSums ? kBuffers : kSums) + 64;
 
@@ -89,7 +88,7 @@ template <int DP> struct Tiles {
     }
 };
 
-// What a block (or a row of attend_join) works on.
+// What a block works on.
 struct Plan {
     int seq, begin, q_len;     // sequence, its first token, its new tokens
     int len;                   // its cached tokens
@@ -111,10 +110,10 @@ __device__ __forceinline__ void row_limits(const AttnParams &p, const Plan &w, i
 }
 
 // Fills in everything of w that follows from seq, begin, q_len, len, row0.
-__device__ __forceinline__ void plan_keys(const AttnParams &p, Plan &w, int group, int max_splits)
+__device__ __forceinline__ void plan_keys(const AttnParams &p, Plan &w, int group, int tile_rows, int max_splits)
 {
     const int left = w.q_len * group - w.row0;
-    w.rows = left < kRowsPerBlock ? left : kRowsPerBlock;
+    w.rows = left < tile_rows ? left : tile_rows;
     int lo, hi, unused;
     row_limits(p, w, w.row0, group, lo, unused);
     row_limits(p, w, w.row0 + w.rows - 1, group, unused, hi);
@@ -139,18 +138,19 @@ __device__ __forceinline__ void plan_sequence(const AttnParams &p, Plan &w, int 
 }
 
 // The sequence and first row of a tile, by the whole wave.  The tiles of
-// sequence s start at off(s) * G / 128 + s: each has room for all of its rows,
+// sequence s start at off(s) * G / tile_rows + s: each has room for all of its rows,
 // and the start grows with s.  Fills in w up to row0; false for a tile that is
 // nobody's.
-__device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile, int group)
+__device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile, int group,
+                                          int tile_rows)
 {
     const PagedParams &g = p.paged;
     const auto off = [&](int i) { return clip(g.q_offsets[i], 0, p.n_tokens); };
-    const auto start = [&](int i) { return int64_t(off(i)) * group / kRowsPerBlock + i; };
+    const auto start = [&](int i) { return int64_t(off(i)) * group / tile_rows + i; };
     const int seq = count_upto(g.n_seqs, tile, start);
     if (seq >= g.n_seqs) return false;
     const int begin = off(seq), end = off(seq + 1);
-    const int64_t row0 = (tile - start(seq)) * kRowsPerBlock;
+    const int64_t row0 = (tile - start(seq)) * tile_rows;
     if (row0 < 0 || row0 >= int64_t(end - begin) * group) return false;
     plan_sequence(p, w, seq, begin, end);
     w.row0 = int(row0);
@@ -257,20 +257,22 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // come, 64 groups at a time.  Groups on no page, or outside [begin, end), are
 // read from page 0 and hidden later, so every read is inside the cache.
 //
-// A tile of 64 keys is shared by four waves, a group each; a tile of 32 is one
-// wave's own.  16-bit caches go straight to LDS, e4m3 ones are read into
-// registers (fetch) and widened on the way to LDS (store).
-template <int DT, int CDT, int DP, bool SHARED>
+// A tile of 64 keys is shared by WAVES waves (four: a group each, eight: half
+// of one); with WAVES = 1 a tile of 32 is a wave's own.  16-bit caches go
+// straight to LDS, e4m3 ones are read into registers (fetch) and widened on
+// the way to LDS (store).  AHEAD: the tile is the last 32 keys of one stride
+// and the first 32 of the next.
+template <int DT, int CDT, int DP, int WAVES, bool AHEAD>
 struct Stage {
     using L = Tiles<DP>;
     using C = typename Elem<CDT>::type;
     static constexpr int VT = Types<DT, CDT>::V;
     static constexpr bool kDirect = CDT != kE4M3;
-    static constexpr int kGroups = SHARED ? 4 : 2;
-    static constexpr int kMine = SHARED ? 1 : 2;                    // groups a wave reads
+    static constexpr int kGroups = WAVES > 1 ? 4 : 2;
+    static constexpr int kMine = WAVES > 1 ? 1 : 2;                 // groups a wave reads of
     static constexpr int kParts = (L::kPieces + 3) / 4;             // 64-lane loads of a group,
     static constexpr bool kHalfPart = L::kPieces % 4 != 0;          // the last one of 32 lanes
-    static constexpr int kLoads = kMine * kParts;                   // a wave's loads of a tile
+    static constexpr int kLoads = kMine * kParts;                   // a wave's loads of a tile, at most
     static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of groups
     static constexpr int kGroupBytes = 16 * L::kRow;
 
@@ -307,7 +309,12 @@ struct Stage {
     {
         const PagedParams &g = p.paged;
         const int lane = int(threadIdx.x) & (kLanes - 1);
-        const int64_t key = first + int64_t(tile + lane / kGroups) * stride + lane % kGroups * 16;
+        int group = lane % kGroups, later = 0;
+        if (AHEAD) {
+            later = group / 2;
+            group ^= 2;
+        }
+        const int64_t key = first + int64_t(tile + lane / kGroups + later) * stride + group * 16;
         int page = -1;
         if (key >= begin && key < end) page = table[key >> g.page_shift];
         if (page >= g.n_pages) page = -1;
@@ -325,6 +332,9 @@ struct Stage {
         return uint32_t(have >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
     }
 
+    // Whether load n of a group is this wave's.
+    __device__ __forceinline__ bool my_part(int n) const { return WAVES < 8 || n % 2 == wave / 4; }
+
     // Issues a tile's reads of keys or of values (to LDS address lds).
     template <bool VALUES>
     __device__ __forceinline__ void fetch(int tile, uint32_t lds)
@@ -333,13 +343,14 @@ struct Stage {
         const bool exact = p.head_dim == DP;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int group = SHARED ? wave : i;
+            const int group = WAVES > 1 ? wave % 4 : i;
             const int from_lane = tile % kBatch * kGroups + group;
             const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), from_lane));
             const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), from_lane));
             const char *base = cache + (hi << 32 | lo);
 #pragma unroll
             for (int n = 0; n < kParts; ++n) {
+                if (!my_part(n)) continue;
                 const uint32_t to = lds + group * kGroupBytes + n * 1024;
                 const int off = offset[VALUES][n];
                 const bool on = !kHalfPart || n + 1 < kParts || (int(threadIdx.x) & 32) == 0;
@@ -367,8 +378,8 @@ struct Stage {
         for (int i = 0; i < kMine; ++i)
 #pragma unroll
             for (int n = 0; n < kParts; ++n) {
-                if (kHalfPart && n + 1 == kParts && lane >= 32) continue;
-                const int id = n * kLanes + lane, group = SHARED ? wave : i;
+                if (!my_part(n) || (kHalfPart && n + 1 == kParts && lane >= 32)) continue;
+                const int id = n * kLanes + lane, group = WAVES > 1 ? wave % 4 : i;
                 f(group * kGroupBytes + id * 16, group * 16 + id / L::kPieces, i * kParts + n);
             }
     }
@@ -383,9 +394,10 @@ struct Stage {
             });
     }
 
-    // Values of places that no row sees become zeros (the tail of a page may
-    // hold anything, and 0 * NaN is not 0); so do infinities and NaN that some
-    // rows see and others do not, which set bad.
+    // Of the pieces this wave has read, before the others see them: values of
+    // places that no row sees become zeros (the tail of a
+    // page may hold anything, and 0 * NaN is not 0); so do infinities and NaN
+    // that some rows see and others do not, which set bad.
     __device__ __forceinline__ void clean_values(char *lds, int tile, uint32_t there, int *bad) const
     {
         const int key0 = first + tile * stride;
@@ -528,7 +540,11 @@ __device__ __forceinline__ void exponentials(f32x16 &s, u32x4 (&w)[2], float &su
         sum += x;
         if (n % 2) {
             const f32x2 pair = {s[n - 1], x};
-            w[n / 8][n / 2 % 4] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, V2));
+            uint32_t both = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, V2));
+            // here, and not where it is used: the compiler would otherwise sink
+            // all of this past the branch that follows the matrix instructions
+            asm volatile("" : "+v"(both), "+v"(sum));
+            w[n / 8][n / 2 % 4] = both;
         }
     }
 }
@@ -636,16 +652,177 @@ struct Parts {
     int64_t rows;         // n_tokens * n_q_heads
 };
 
+// The keys [from, to) of a tile by waves that own 32 rows each and share the
+// keys in WAYS ways: way y takes keys from + 64 (WAYS t + y) in turn t.
+//
+// A turn is 64 keys in two halves.  While a wave turns the scores of 32 keys
+// into weights, the matrix cores compute the scores of the next 32; while they
+// add its values, it finds the next maximum.  Keys are therefore wanted half a
+// turn before their values, and the key tiles in LDS lie half a turn ahead.
+// Two buffers each; a turn's reads run for the whole turn before it.
+template <int DT, int CDT, int DP, int WAYS>
+__device__ __forceinline__ void walk_rows(const AttnParams &p, const Plan &w, int kv_head, int group,
+                                          int wave, int from, int to, int lo, int hi, float c,
+                                          const u32x4 (&q)[Tiles<DP>::kSteps], char *lds, int *bad,
+                                          Rows<DP> &r)
+{
+    using L = Tiles<DP>;
+    constexpr int VT = Types<DT, CDT>::V, kWaves = L::kWaves / WAYS;
+    constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf, kStride = 64 * WAYS;
+    using Keys = Stage<DT, CDT, DP, kWaves, true>;
+    using Vals = Stage<DT, CDT, DP, kWaves, false>;
+    const int way = wave / kWaves, first = from + way * 64;
+    lds += way * 4 * kTile;
+    const uint32_t at = lds_address(lds);
+    Keys sk(p, w, kv_head, wave % kWaves, first - kStride, kStride, from, to);   // tile t + 1: after turn t
+    Vals sv(p, w, kv_head, wave % kWaves, first, kStride, from, to);
+
+    // limits of all of the wave's rows (they grow with the row), and of the tile's
+    const int wave_lo = __builtin_amdgcn_readlane(lo, 0);
+    const int wave_hi = min(__builtin_amdgcn_readlane(hi, 31), to);
+    const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
+    const int plain_hi = min(__builtin_amdgcn_readlane(hi, 0), to) - 32;
+    // keys that every row of the tile sees; elsewhere values are looked at
+    int blo, bhi, unused;
+    row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
+    row_limits(p, w, w.row0, group, unused, bhi);
+    bhi = min(bhi, to);
+
+    const int n_turns = (to - from + kStride - 1) / kStride;
+    const auto sees = [&](int t) {
+        const int key0 = first + t * kStride;
+        return t >= 0 && t < n_turns && key0 < wave_hi && key0 + 64 > wave_lo;
+    };
+    const auto hidden = [&](int key0, uint32_t there, f32x16 &y) {
+        if (key0 >= plain_lo && key0 <= plain_hi && there == 3) return;
+        hide(y, lo - key0, min(hi, to) - key0, there);
+    };
+    const auto read_keys = [&](int t) {       // the second half of turn t, the first of t + 1
+        if ((t + 1) % Keys::kBatch == 0) sk.find_pages(t + 1);
+        sk.template fetch<false>(t + 1, at + ((t + 1) & 1) * kTile);
+    };
+
+    f32x16 a = 0.0f, b = 0.0f;                // scores of a turn's halves
+    u32x4 x[2];
+    float top = -INFINITY, none = 0.0f;
+    uint32_t next_there = 0;                  // groups of the next turn that are on a page
+    if (n_turns > 0) read_keys(-1);
+    for (int t = -1; t < n_turns; ++t) {
+        char *keys = lds + ((t + 1) & 1) * kTile, *values = lds + (2 + (t & 1)) * kTile;
+        const int key0 = first + t * kStride;
+        const uint32_t there = next_there;
+        if constexpr (Keys::kDirect) {
+            wait_loads<0>();
+        } else {
+            sk.template store<false>(keys);
+            if (t >= 0) sv.template store<true>(values);
+        }
+        if (t >= 0 && (key0 < blo || key0 + 64 > bhi || there != 15))
+            sv.clean_values(values, t, there, bad);
+        __syncthreads();
+        // every wave is done with the last turn's buffers
+        if (t + 1 < n_turns) {
+            if ((t + 1) % Vals::kBatch == 0) sv.find_pages(t + 1);
+            next_there = sv.groups_there(t + 1);
+            sv.template fetch<true>(t + 1, at + (2 + ((t + 1) & 1)) * kTile);
+            read_keys(t + 1);
+        }
+        const bool more = sees(t + 1);
+        if (sees(t)) {
+            float base = move_top<DP>(r, both_halves(top), c);
+            scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, base);
+            Ready<DP> ready = read_ahead<DP>(values);
+            hidden(key0 + 32, there >> 2, b);
+            in_order();
+            add_values<VT, DP, true>(r, x, values, ready, b, top);
+            base = move_top<DP>(r, both_halves(top), c);
+            // in the last turn the next scores are of keys that nobody wants,
+            // and so is their maximum
+            scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, base);
+            ready = read_ahead<DP>(values + kHalf);
+            if (more) hidden(key0 + kStride, next_there & 3, a);
+            in_order();
+            add_values<VT, DP, true>(r, x, values + kHalf, ready, a, top);
+        } else if (more) {
+            scores<DT, VT, DP, false>(a, q, keys + kHalf, b, x, none, c, 0.0f);
+            hidden(key0 + kStride, next_there & 3, a);
+            top = largest(a);
+        }
+    }
+}
+
+// The keys [from, to) of a tile whose rows every wave has: a wave takes every
+// kWaves-th 32 keys.  It has a buffer of its own: the next keys are read once
+// the scores are done with these, the next values once O is.
 template <int DT, int CDT, int DP>
-__global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p, Parts parts,
-                                                                   int tiles, int max_splits)
+__device__ __forceinline__ void walk_keys(const AttnParams &p, const Plan &w, int kv_head, int wave,
+                                          int from, int to, int lo, int hi, float c,
+                                          const u32x4 (&q)[Tiles<DP>::kSteps], char *lds, int *bad,
+                                          Rows<DP> &r)
+{
+    using L = Tiles<DP>;
+    using S = Stage<DT, CDT, DP, 1, false>;
+    constexpr int VT = Types<DT, CDT>::V;
+    constexpr int kStep = 32 * L::kWaves, kHalf = 32 * L::kRow;
+    const int first = from + wave * 32;
+    S st(p, w, kv_head, 0, first, kStep, from, to);
+    char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
+    const uint32_t keys_at = lds_address(keys), values_at = keys_at + kHalf;
+    const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
+    const int plain_hi = min(__builtin_amdgcn_readlane(hi, 0), to) - 32;
+    const int n_tiles = to > first ? (to - first + kStep - 1) / kStep : 0;
+    if (n_tiles > 0) {
+        st.find_pages(0);
+        st.template fetch<false>(0, keys_at);
+        st.template fetch<true>(0, values_at);
+    }
+    for (int t = 0; t < n_tiles; ++t) {
+        const int key0 = first + t * kStep;
+        const bool more = t + 1 < n_tiles;
+        const uint32_t there = st.groups_there(t);
+        f32x16 s;
+        u32x4 x[2];
+        float unused;
+        if constexpr (S::kDirect) {
+            wait_loads<S::kLoads>();                 // the values may be on their way
+        } else {
+            st.template store<false>(keys);
+            st.template store<true>(values);
+        }
+        scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f);
+        if (more) {
+            if ((t + 1) % S::kBatch == 0) st.find_pages(t + 1);
+            wait_lds();
+            st.template fetch<false>(t + 1, keys_at);
+            if constexpr (!S::kDirect) st.template fetch<true>(t + 1, values_at);
+        }
+        const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
+        if (!whole) hide(s, lo - key0, min(hi, to) - key0, there);
+        const float base = move_top<DP>(r, both_halves(largest(s)), c);
+        exponentials<VT>(s, x, r.sum, c, base, 0, 16);
+        if constexpr (S::kDirect) {
+            if (more) wait_loads<S::kLoads>();
+            else wait_loads<0>();
+        }
+        if (!whole) st.clean_values(values, t, there, bad);
+        add_values<VT, DP, false>(r, x, values, read_ahead<DP>(values), s, unused);
+        if constexpr (S::kDirect) {
+            wait_lds();
+            if (more) st.template fetch<true>(t + 1, values_at);
+        }
+    }
+}
+
+template <int DT, int CDT, int DP>
+__global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void attend(
+    AttnParams p, Parts parts, int tiles, int tile_rows, int max_splits)
 {
     using T = typename Elem<DT>::type;
     using L = Tiles<DP>;
-    constexpr int VT = Types<DT, CDT>::V;
+    constexpr int kWaves = L::kWaves;
     __shared__ __attribute__((aligned(16))) char lds[L::kLds];
     __shared__ int bad;          // a hidden place may hold a value that is not finite
-    __shared__ float wave_stats[kWavesPerBlock][32][2];
+    __shared__ float wave_stats[kWaves][32][2];
 
     const PagedParams &g = p.paged;
     const int lane = int(threadIdx.x) & (kLanes - 1);
@@ -659,15 +836,18 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     const int split = int(blockIdx.y);
 
     Plan w;
-    if (!find_tile(p, w, tile, group)) return;
-    plan_keys(p, w, group, max_splits);
+    if (!find_tile(p, w, tile, group, tile_rows)) return;
+    plan_keys(p, w, group, tile_rows, max_splits);
     if (split >= w.splits) return;
     const int from = w.lo + split * w.per;
     const int to = min(w.hi, from + w.per);
-    const bool by_keys = w.rows <= kRowsPerWave;
+    // waves that share their rows: all, two and two, or none
+    const int ways = w.rows <= kRowsPerWave ? kWaves
+                     : (kWaves == 8 && w.rows <= 4 * kRowsPerWave ? 2 : 1);
+    const int row_waves = kWaves / ways;
 
     // this lane's row, its limits, and its queries (rows past the last repeat it)
-    const int first = by_keys ? 0 : wave * kRowsPerWave;
+    const int first = wave % row_waves * kRowsPerWave;
     const int row = w.row0 + min(first + col, w.rows - 1);
     const int token = w.begin + row / group, head = kv_head * group + row % group;
     int lo, hi;
@@ -684,9 +864,6 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
 #pragma unroll
         for (int st = 0; st < L::kSteps; ++st) asm volatile("" : "+v"(q[st]));
     }
-    // limits of all of the wave's rows (they grow with the row)
-    const int wave_lo = __builtin_amdgcn_readlane(lo, 0), wave_hi = __builtin_amdgcn_readlane(hi, 31);
-    const int all_lo = __builtin_amdgcn_readlane(lo, 31), all_hi = __builtin_amdgcn_readlane(hi, 0);
     const float c = p.scale * g.k_scale * kLog2e;
 
     if (threadIdx.x == 0) bad = 0;
@@ -697,145 +874,17 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
 #pragma unroll
     for (int dt = 0; dt < L::kDims; ++dt) r.o[dt] = 0.0f;
 
-    const uint32_t at = lds_address(lds);
-    if (!by_keys) {
-        // Turns of 64 keys in two halves.  While a wave turns the scores of 32
-        // keys into weights, the matrix cores compute the scores of the next
-        // 32; while they add its values, it finds the next maximum.  Keys are
-        // therefore wanted half a turn before their values: the key tiles in
-        // LDS lie 32 keys further on.  Two buffers each; a turn's reads run
-        // for the whole turn before it.
-        using S = Stage<DT, CDT, DP, true>;
-        S sk(p, w, kv_head, wave, from + 32, 64, from, to), sv(p, w, kv_head, wave, from, 64, from, to);
-        constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf;
-        // keys that every row of the block sees; elsewhere values are looked at
-        int blo, bhi, unused;
-        row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
-        row_limits(p, w, w.row0, group, unused, bhi);
-        bhi = min(bhi, to);
-        const int n_turns = (to - from + 63) / 64;
-        // turns [mine, done) have keys that a row of this wave sees
-        const int mine = max(wave_lo - from, 0) / 64, done = (min(wave_hi, to) - from + 63) >> 6;
-        const int plain_lo = all_lo, plain_hi = min(all_hi, to) - 32;
-        uint32_t now_there = 0, next_there = 0;        // groups of this turn, of the next
-        const auto pages_of = [&](int t) {
-            if (t % S::kBatch == 0) sv.find_pages(t);
-            return sv.groups_there(t);
-        };
-        const auto hidden = [&](int key0, uint32_t there, f32x16 &y) {
-            if (key0 >= plain_lo && key0 <= plain_hi && there == 3) return;
-            hide(y, lo - key0, min(hi, to) - key0, there);
-        };
-        // key tile t: keys 32-63 of turn t, then 0-31 of turn t + 1
-        const auto read_keys = [&](int t) {
-            if ((t + 1) % S::kBatch == 0) sk.find_pages(t + 1);
-            sk.template fetch<false>(t + 1, at + ((t + 1) & 1) * kTile);
-        };
-        sk.first -= 64;                                // its tile 0 is key tile -1
-        f32x16 a = 0.0f, b = 0.0f;                     // scores of a turn's halves
-        u32x4 x[2];
-        float top = -INFINITY, none = 0.0f;
-        if (n_turns > 0) read_keys(-1);
-        for (int t = -1; t < n_turns; ++t) {
-            char *keys = lds + ((t + 1) & 1) * kTile, *values = lds + (2 + (t & 1)) * kTile;
-            if constexpr (S::kDirect) {
-                wait_loads<0>();
-            } else {
-                sk.template store<false>(keys);
-                if (t >= 0) sv.template store<true>(values);
-            }
-            __syncthreads();
-            // every wave is done with the last turn's buffers
-            now_there = next_there;
-            if (t + 1 < n_turns) {
-                next_there = pages_of(t + 1);
-                sv.template fetch<true>(t + 1, at + (2 + ((t + 1) & 1)) * kTile);
-                read_keys(t + 1);
-            }
-            const int key0 = from + t * 64;
-            if (t >= 0 && (key0 < blo || key0 + 64 > bhi || now_there != 15)) {
-                sv.clean_values(values, t, now_there, &bad);
-                __syncthreads();
-            }
-            const bool more = t + 1 >= mine && t + 1 < done;
-            if (t >= mine && t < done && t >= 0) {
-                float base = move_top<DP>(r, both_halves(top), c);
-                scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, base);
-                Ready<DP> ready = read_ahead<DP>(values);
-                hidden(key0 + 32, now_there >> 2, b);
-                in_order();
-                add_values<VT, DP, true>(r, x, values, ready, b, top);
-                base = move_top<DP>(r, both_halves(top), c);
-                // the last turn has no next scores: its maximum is then of old
-                // ones, and nobody asks for it
-                if (more) scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, base);
-                else exponentials<VT>(b, x, r.sum, c, base, 0, 16);
-                ready = read_ahead<DP>(values + kHalf);
-                if (more) hidden(key0 + 64, next_there & 3, a);
-                in_order();
-                add_values<VT, DP, true>(r, x, values + kHalf, ready, a, top);
-            } else if (more) {
-                scores<DT, VT, DP, false>(a, q, keys + kHalf, b, x, none, c, 0.0f);
-                hidden(key0 + 64, next_there & 3, a);
-                top = largest(a);
-            }
-        }
-    } else {
-        // a buffer of 32 keys for each wave: the next keys are read once the
-        // scores are done with these, the next values once O is
-        using S = Stage<DT, CDT, DP, false>;
-        constexpr int kStep = 32 * kWavesPerBlock;
-        constexpr int kHalf = 32 * L::kRow;
-        const int first_key = from + wave * 32;
-        S st(p, w, kv_head, 0, first_key, kStep, from, to);
-        char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
-        const uint32_t keys_at = at + wave * 2 * kHalf, values_at = keys_at + kHalf;
-        const int n_tiles = to > first_key ? (to - first_key + kStep - 1) / kStep : 0;
-        if (n_tiles > 0) {
-            st.find_pages(0);
-            st.template fetch<false>(0, keys_at);
-            st.template fetch<true>(0, values_at);
-        }
-        for (int tile = 0; tile < n_tiles; ++tile) {
-            const int key0 = first_key + tile * kStep;
-            const bool more = tile + 1 < n_tiles;
-            const uint32_t there = st.groups_there(tile);
-            f32x16 s;
-            u32x4 x[2];
-            float unused;
-            if constexpr (S::kDirect) {
-                wait_loads<S::kLoads>();                 // the values may be on their way
-            } else {
-                st.template store<false>(keys);
-                st.template store<true>(values);
-            }
-            scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f);
-            if (more) {
-                if ((tile + 1) % S::kBatch == 0) st.find_pages(tile + 1);
-                wait_lds();
-                st.template fetch<false>(tile + 1, keys_at);
-                if constexpr (!S::kDirect) st.template fetch<true>(tile + 1, values_at);
-            }
-            const bool whole = key0 >= all_lo && key0 + 32 <= min(all_hi, to) && there == 3;
-            if (!whole) hide(s, lo - key0, min(hi, to) - key0, there);
-            const float base = move_top<DP>(r, both_halves(largest(s)), c);
-            exponentials<VT>(s, x, r.sum, c, base, 0, 16);
-            if constexpr (S::kDirect) {
-                if (more) wait_loads<S::kLoads>();
-                else wait_loads<0>();
-            }
-            if (!whole) st.clean_values(values, tile, there, &bad);
-            add_values<VT, DP, false>(r, x, values, read_ahead<DP>(values), s, unused);
-            if constexpr (S::kDirect) {
-                wait_lds();
-                if (more) st.template fetch<true>(tile + 1, values_at);
-            }
-        }
-    }
+    if (ways == 1)
+        walk_rows<DT, CDT, DP, 1>(p, w, kv_head, group, wave, from, to, lo, hi, c, q, lds, &bad, r);
+    else if (ways == 2)
+        walk_rows<DT, CDT, DP, kWaves == 8 ? 2 : 1>(p, w, kv_head, group, wave, from, to, lo, hi, c, q,
+                                                    lds, &bad, r);
+    else
+        walk_keys<DT, CDT, DP>(p, w, kv_head, wave, from, to, lo, hi, c, q, lds, &bad, r);
     r.sum += __shfl_xor(r.sum, 32);
 
-    // Every wave's O goes through LDS, so that stores are whole rows; the
-    // waves of a tile by keys bring theirs to a common maximum and are added.
+    // Every wave's O goes through LDS, so that stores are whole rows; waves
+    // with the same rows bring theirs to a common maximum and are added.
     if (half == 0) {
         wave_stats[wave][col][0] = r.top;
         wave_stats[wave][col][1] = r.sum;
@@ -848,10 +897,9 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     float *all = reinterpret_cast<float *>(lds);      // [wave][row][kRow]
     if (first + col < w.rows) {
         float keep = 1.0f;
-        if (by_keys) {
+        if (ways > 1) {
             float top = r.top;
-#pragma unroll
-            for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, wave_stats[i][col][0]);
+            for (int i = wave % row_waves; i < kWaves; i += row_waves) top = fmaxf(top, wave_stats[i][col][0]);
             keep = weight(r.top, top);
         }
 #pragma unroll
@@ -866,27 +914,18 @@ __global__ __launch_bounds__(kBlock, DP > 128 ? 1 : 2) void attend(AttnParams p,
     }
     __syncthreads();
     const int fours = p.head_dim / 4;
-    for (int i = int(threadIdx.x); i < w.rows * fours; i += kBlock) {
+    for (int i = int(threadIdx.x); i < w.rows * fours; i += kWaves * kLanes) {
         const int n = i / fours, d = (i - n * fours) * 4;
-        f32x4 x;
-        float top, sum;
-        if (by_keys) {
-            x = 0.0f;
-            top = -INFINITY;
-            sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kWavesPerBlock; ++k) {
-                x += *reinterpret_cast<const f32x4 *>(all + (k * 32 + n) * kRow + d);
-                top = fmaxf(top, wave_stats[k][n][0]);
-            }
-#pragma unroll
-            for (int k = 0; k < kWavesPerBlock; ++k)
-                if (wave_stats[k][n][1] != 0.0f)
-                    sum += wave_stats[k][n][1] * weight(wave_stats[k][n][0], top);
-        } else {
-            x = *reinterpret_cast<const f32x4 *>(all + n * kRow + d);
-            top = wave_stats[n / 32][n % 32][0];
-            sum = wave_stats[n / 32][n % 32][1];
+        f32x4 x = 0.0f;
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = n / 32; k < kWaves; k += row_waves) {
+            x += *reinterpret_cast<const f32x4 *>(all + (k * 32 + n % 32) * kRow + d);
+            top = fmaxf(top, wave_stats[k][n % 32][0]);
+        }
+        for (int k = n / 32; k < kWaves; k += row_waves) {
+            const float part = wave_stats[k][n % 32][1];
+            if (ways == 1) sum = part;
+            else if (part != 0.0f) sum += part * weight(wave_stats[k][n % 32][0], top);
         }
         const int row = w.row0 + n;
         const int64_t t = w.begin + row / group;
@@ -926,15 +965,16 @@ __device__ __forceinline__ float part_weight(float top, float all)
 }
 
 template <int DT>
-__global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts parts, int max_splits)
+__global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts parts, int tile_rows,
+                                                          int max_splits)
 {
     using T = typename Elem<DT>::type;
     __shared__ Sum shared[kJoinBlock];
     const int group = p.n_q_heads / p.n_k_heads;
     const int kv_head = int(blockIdx.x) % p.n_k_heads;
     Plan w;
-    if (!find_tile(p, w, int(blockIdx.x) / p.n_k_heads, group)) return;
-    plan_keys(p, w, group, max_splits);
+    if (!find_tile(p, w, int(blockIdx.x) / p.n_k_heads, group, tile_rows)) return;
+    plan_keys(p, w, group, tile_rows, max_splits);
     if (w.splits == 1) return;
 
     const int turn = int(gridDim.y), rows = (w.rows - int(blockIdx.y) + turn - 1) / turn;
@@ -984,29 +1024,30 @@ __global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts pa
     put(row_of(i), i % fours * 4, a);
 }
 
-// Parts of the launch: tiles of 128 rows (an upper bound that needs no look
-// at the offsets) and splits of the keys.
-struct Shape { int64_t tiles; int splits; };
+// Parts of the launch: rows of a tile, tiles (an upper bound that needs no
+// look at the offsets) and splits of the keys.
+struct Shape { int tile_rows; int64_t tiles; int splits; };
 
 Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_heads,
                int32_t head_dim, int32_t page_size, int32_t max_pages)
 {
-    const int64_t group = n_q_heads / n_k_heads;
+    const int64_t group = n_q_heads / n_k_heads, rows = n_tokens * group;
+    const int64_t slots = 256;           // blocks the chip holds: one for each CU
     Shape s;
-    s.tiles = n_tokens * group / kRowsPerBlock + n_seqs;
+    s.tile_rows = head_dim <= 128 && rows / 256 * n_k_heads >= 2 * slots ? 256 : 128;
+    s.tiles = rows / s.tile_rows + n_seqs;
     const int64_t blocks = s.tiles * n_k_heads;
     const int64_t units = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
-    const int64_t slots = head_dim > 128 ? 256 : 512;        // blocks the chip holds
     s.splits = 1;
-    if (blocks == 0 || units <= 4) return s;
-    if (n_tokens * group <= int64_t(n_seqs) * kRowsPerWave) {
+    if (blocks == 0 || units <= 2) return s;
+    if (rows <= int64_t(n_seqs) * kRowsPerWave) {
         // few rows: the keys are read once and HBM decides.  Enough blocks to
-        // fill the chip, and then more while each still has 8 units, so that
+        // fill the chip, and then more while each still has 4 units, so that
         // sequences of different lengths end together
         int64_t n = slots / blocks;
-        if (n * kMinUnits > units) n = units / kMinUnits;
-        int64_t fine = 4096 / blocks;
-        if (fine * 8 > units) fine = units / 8;
+        if (n > units) n = units;
+        int64_t fine = 2048 / blocks;
+        if (fine * 4 > units) fine = units / 4;
         n = n > fine ? n : fine;
         n = n < 256 ? n : 256;
         s.splits = int(n < 1 ? 1 : n);
@@ -1014,8 +1055,8 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
     }
     // many rows: the blocks run in rounds of `slots`; a split costs about two
     // units more in each block and, where there are any, four for the join
-    const int64_t full = (n_tokens * group + (n_seqs - 1) * (kRowsPerBlock / 2) + kRowsPerBlock - 1) /
-                         kRowsPerBlock * n_k_heads;        // about the tiles that have rows
+    const int64_t full = (rows + (n_seqs - 1) * (s.tile_rows / 2) + s.tile_rows - 1) / s.tile_rows *
+                         n_k_heads;                        // about the tiles that have rows
     int64_t best = INT64_MAX;
     for (int n = 1; n <= 8 && n * kMinUnits <= units; ++n) {
         const int64_t cost = (full * n + slots - 1) / slots * ((units + n - 1) / n + 2) + (n > 1 ? 4 : 0);
@@ -1029,19 +1070,25 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
 
 size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
 
+template <int DT, int CDT, int DP>
+void launch(const AttnParams &p, const Parts &parts, const Shape &s, hipStream_t stream)
+{
+    const dim3 grid(uint32_t(s.tiles * p.n_k_heads), uint32_t(s.splits));
+    attend<DT, CDT, DP><<<grid, Tiles<DP>::kWaves * kLanes, 0, stream>>>(p, parts, int(s.tiles),
+                                                                         s.tile_rows, s.splits);
+}
+
 template <int DT, int CDT>
 void launch_attend(const AttnParams &p, const Parts &parts, const Shape &s, hipStream_t stream)
 {
-    const dim3 grid(uint32_t(s.tiles * p.n_k_heads), uint32_t(s.splits));
-    const int tiles = int(s.tiles);
     const int d = p.head_dim;
-    if (d <= 32) attend<DT, CDT, 32><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else if (d <= 64) attend<DT, CDT, 64><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else if (d <= 80) attend<DT, CDT, 80><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else if (d <= 96) attend<DT, CDT, 96><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else if (d <= 128) attend<DT, CDT, 128><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else if (d <= 192) attend<DT, CDT, 192><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
-    else attend<DT, CDT, 256><<<grid, kBlock, 0, stream>>>(p, parts, tiles, s.splits);
+    if (d <= 32) launch<DT, CDT, 32>(p, parts, s, stream);
+    else if (d <= 64) launch<DT, CDT, 64>(p, parts, s, stream);
+    else if (d <= 80) launch<DT, CDT, 80>(p, parts, s, stream);
+    else if (d <= 96) launch<DT, CDT, 96>(p, parts, s, stream);
+    else if (d <= 128) launch<DT, CDT, 128>(p, parts, s, stream);
+    else if (d <= 192) launch<DT, CDT, 192>(p, parts, s, stream);
+    else launch<DT, CDT, 256>(p, parts, s, stream);
 }
 
 }  // namespace
@@ -1074,8 +1121,8 @@ hipError_t run_paged_attention(const AttnParams &p, hipStream_t stream)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1) return e;
     const dim3 blocks(uint32_t(s.tiles * p.n_k_heads), s.splits >= 16 ? 8 : 1);
-    if (p.dtype == kF16) attend_join<kF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.splits);
-    else attend_join<kBF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.splits);
+    if (p.dtype == kF16) attend_join<kF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.tile_rows, s.splits);
+    else attend_join<kBF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.tile_rows, s.splits);
     return hipGetLastError();
 }
 

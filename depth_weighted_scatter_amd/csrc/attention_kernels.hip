@@ -157,11 +157,19 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile
     return true;
 }
 
-// One wave's rows: their part of O^T, running maximum of the scores (before
-// the scale) and this lane's part of the weights' sum.
+// One wave's rows: their part of O^T, the reference maximum of the scores
+// (before the scale) with what follows from it, and this lane's part of the
+// weights' sum.
 template <int DP> struct Rows {
     f32x16 o[Tiles<DP>::kDims];
-    float top, sum;
+    float top, base, limit;     // reference; times c (0 without one); past this it moves
+    float sum;
+
+    __device__ Rows() : top(-INFINITY), base(0.0f), limit(-INFINITY), sum(0.0f)
+    {
+#pragma unroll
+        for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) o[dt] = 0.0f;
+    }
 };
 
 // 16-bit values with all exponent bits set (infinity, NaN) in a dword pair.
@@ -262,7 +270,7 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // straight to LDS, e4m3 ones are read into registers (fetch) and widened on
 // the way to LDS (store).  AHEAD: the tile is the last 32 keys of one stride
 // and the first 32 of the next.
-template <int DT, int CDT, int DP, int WAVES, bool AHEAD>
+template <int DT, int CDT, int DP, bool EXACT, int WAVES, bool AHEAD>
 struct Stage {
     using L = Tiles<DP>;
     using C = typename Elem<CDT>::type;
@@ -272,7 +280,9 @@ struct Stage {
     static constexpr int kMine = WAVES > 1 ? 1 : 2;                 // groups a wave reads of
     static constexpr int kParts = (L::kPieces + 3) / 4;             // 64-lane loads of a group,
     static constexpr bool kHalfPart = L::kPieces % 4 != 0;          // the last one of 32 lanes
-    static constexpr int kLoads = kMine * kParts;                   // a wave's loads of a tile, at most
+    static constexpr int kHalves = WAVES == 8 ? 2 : 1;              // waves that share a group
+    static constexpr int kSlots = (kParts + kHalves - 1) / kHalves; // a wave's loads of a group,
+    static constexpr int kLoads = kMine * kSlots;                   // of a tile
     static constexpr int kBatch = kLanes / kGroups;                 // tiles of a batch of groups
     static constexpr int kGroupBytes = 16 * L::kRow;
 
@@ -283,7 +293,7 @@ struct Stage {
     int row_bytes;
     uint32_t group_lo, group_hi;               // lane's group: its byte offset in the cache
     uint64_t have;                             // groups that are on a page
-    int offset[2][kParts];                     // lane's pieces: bytes from their group, -1 for a zero
+    int offset[2][kSlots];                     // lane's pieces: bytes from their group, -1 for a zero
     u32x2 k[kDirect ? 1 : kLoads], v[kDirect ? 1 : kLoads];
 
     __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
@@ -293,8 +303,8 @@ struct Stage {
           row_bytes(p.head_dim * int(sizeof(C)))
     {
 #pragma unroll
-        for (int n = 0; n < kParts; ++n) {
-            const int id = n * kLanes + (int(threadIdx.x) & (kLanes - 1));
+        for (int n = 0; n < kSlots; ++n) {
+            const int id = part(n) * kLanes + (int(threadIdx.x) & (kLanes - 1));
             const int key = id / L::kPieces, at = id % L::kPieces;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -332,44 +342,54 @@ struct Stage {
         return uint32_t(have >> (tile % kBatch * kGroups)) & ((1u << kGroups) - 1);
     }
 
-    // Whether load n of a group is this wave's.
-    __device__ __forceinline__ bool my_part(int n) const { return WAVES < 8 || n % 2 == wave / 4; }
-
-    // Issues a tile's reads of keys or of values (to LDS address lds).
-    template <bool VALUES>
-    __device__ __forceinline__ void fetch(int tile, uint32_t lds)
+    // The part of a group that this wave's load n brings, and whether the lane
+    // has a piece of it.
+    __device__ __forceinline__ int part(int n) const { return n * kHalves + (kHalves > 1 ? wave / 4 : 0); }
+    __device__ __forceinline__ bool has_piece(int n) const
     {
-        const char *cache = static_cast<const char *>(VALUES ? p.paged.v_cache : p.paged.k_cache);
-        const bool exact = p.head_dim == DP;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int group = WAVES > 1 ? wave % 4 : i;
-            const int from_lane = tile % kBatch * kGroups + group;
-            const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), from_lane));
-            const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), from_lane));
-            const char *base = cache + (hi << 32 | lo);
-#pragma unroll
-            for (int n = 0; n < kParts; ++n) {
-                if (!my_part(n)) continue;
-                const uint32_t to = lds + group * kGroupBytes + n * 1024;
-                const int off = offset[VALUES][n];
-                const bool on = !kHalfPart || n + 1 < kParts || (int(threadIdx.x) & 32) == 0;
-                if constexpr (kDirect) {
-                    if (!on) continue;
-                    if (exact)
-                        load_to_lds(base, uint32_t(off), to);
-                    else
-                        load_to_lds(off < 0 ? reinterpret_cast<const char *>(&kZeroPiece) : base + off, to);
-                } else {
-                    u32x2 x = 0u;
-                    if (on && off >= 0) x = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
-                    (VALUES ? v : k)[i * kParts + n] = x;
-                }
-            }
+        if constexpr (kParts % kHalves == 0 && !kHalfPart) return true;
+        else return part(n) * kLanes + (int(threadIdx.x) & (kLanes - 1)) < 16 * L::kPieces;
+    }
+
+    // Where the wave's i-th group of a tile lies in a cache.
+    __device__ __forceinline__ const char *group_at(const void *cache, int tile, int i) const
+    {
+        const int lane = tile % kBatch * kGroups + (WAVES > 1 ? wave % 4 : i);
+        const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(group_lo), lane));
+        const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(group_hi), lane));
+        return static_cast<const char *>(cache) + (hi << 32 | lo);
+    }
+
+    // Issues load n of the wave's i-th group, of keys or of values, to the
+    // tile at LDS address lds.
+    template <bool VALUES>
+    __device__ __forceinline__ void fetch_part(const char *base, int i, int n, uint32_t lds)
+    {
+        const uint32_t to = lds + (WAVES > 1 ? wave % 4 : i) * kGroupBytes + part(n) * 1024;
+        const int off = offset[VALUES][n];
+        if constexpr (kDirect) {
+            if (!has_piece(n)) return;
+            if constexpr (EXACT) load_to_lds(base, uint32_t(off), to);
+            else load_to_lds(off < 0 ? reinterpret_cast<const char *>(&kZeroPiece) : base + off, to);
+        } else {
+            u32x2 x = 0u;
+            if (has_piece(n) && (EXACT || off >= 0)) x = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
+            (VALUES ? v : k)[i * kSlots + n] = x;
         }
     }
 
-    // Calls f(byte in the tile, key) for each of this lane's pieces.
+    template <bool VALUES>
+    __device__ __forceinline__ void fetch(int tile, uint32_t lds)
+    {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const char *base = group_at(VALUES ? p.paged.v_cache : p.paged.k_cache, tile, i);
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n) fetch_part<VALUES>(base, i, n, lds);
+        }
+    }
+
+    // Calls f(byte in the tile, key, register) for each of this lane's pieces.
     template <typename F>
     __device__ __forceinline__ void each_piece(F f) const
     {
@@ -377,10 +397,10 @@ struct Stage {
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
 #pragma unroll
-            for (int n = 0; n < kParts; ++n) {
-                if (!my_part(n) || (kHalfPart && n + 1 == kParts && lane >= 32)) continue;
-                const int id = n * kLanes + lane, group = WAVES > 1 ? wave % 4 : i;
-                f(group * kGroupBytes + id * 16, group * 16 + id / L::kPieces, i * kParts + n);
+            for (int n = 0; n < kSlots; ++n) {
+                if (!has_piece(n)) continue;
+                const int id = part(n) * kLanes + lane, group = WAVES > 1 ? wave % 4 : i;
+                f(group * kGroupBytes + id * 16, group * 16 + id / L::kPieces, i * kSlots + n);
             }
     }
 
@@ -505,17 +525,19 @@ __device__ __forceinline__ float both_halves(float x)
                                          __builtin_bit_cast(float, uint32_t(r[1])));
 }
 
-// Takes a tile's largest score into the running maximum.  The reference moves
-// only when a row's weights would pass 2^8: any reference within that of the
-// true maximum gives the same softmax, and most tiles then leave O as it is.
-// Returns the reference times c (0 while no key has been seen).
+// Takes the largest of a lane's scores into the running maximum.  The
+// reference moves only when a weight would pass 2^8: any reference within that
+// of the true maximum gives the same softmax, and most tiles then leave O as
+// it is, and ask no other lane.
 template <int DP>
-__device__ __forceinline__ float move_top(Rows<DP> &r, float top, float c)
+__device__ __forceinline__ void move_top(Rows<DP> &r, float top, float c)
 {
-    if (__any(top * c > r.top * c + 8.0f || (r.top == -INFINITY && top > -INFINITY))) {
-        const float now = fmaxf(r.top, top);
+    if (__any(top > r.limit)) {
+        const float now = fmaxf(r.top, both_halves(top));
         const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
         r.top = now;
+        r.base = now == -INFINITY ? 0.0f : now * c;
+        r.limit = now + 8.0f / c;
         r.sum *= keep;
 #pragma unroll
         for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) {
@@ -523,7 +545,6 @@ __device__ __forceinline__ float move_top(Rows<DP> &r, float top, float c)
             in_order();
         }
     }
-    return r.top == -INFINITY ? 0.0f : r.top * c;
 }
 
 // Scores [from, to) of 32 keys to weights, added to sum; pairs are rounded to
@@ -549,13 +570,19 @@ __device__ __forceinline__ void exponentials(f32x16 &s, u32x4 (&w)[2], float &su
     }
 }
 
+// No loads beside a run of matrix instructions.
+struct NoLoads {
+    __device__ __forceinline__ void operator()(int, int) const {}
+};
+
 // S^T of 32 keys.  The matrix instructions run beside the exponentials of the
 // 32 keys before (BESIDE): a wave issues one and goes on, and 16 scores take
-// about as long as the head's instructions do.
-template <int DT, int VT, int DP, bool BESIDE>
+// about as long as the head's instructions do; loads(n, kN) issues what is to be
+// issued beside the n-th of kN.
+template <int DT, int VT, int DP, bool BESIDE, typename Loads>
 __device__ __forceinline__ void scores(f32x16 &out, const u32x4 (&q)[Tiles<DP>::kSteps],
                                        const char *keys, f32x16 &s, u32x4 (&w)[2], float &sum, float c,
-                                       float base)
+                                       float base, Loads loads)
 {
     constexpr int kN = Tiles<DP>::kSteps, kAhead = kN < 4 ? kN : 4;
     const KeyReads<DP> read(keys);
@@ -569,6 +596,7 @@ __device__ __forceinline__ void scores(f32x16 &out, const u32x4 (&q)[Tiles<DP>::
         o = mfma<DT>(a[n % kAhead], q[n], o);
         if (n + kAhead < kN) a[n % kAhead] = read(n + kAhead);
         if constexpr (BESIDE) exponentials<VT>(s, w, sum, c, base, n * 16 / kN, (n + 1) * 16 / kN);
+        loads(n, kN);
         in_order();
     }
     out = o;
@@ -592,9 +620,9 @@ __device__ __forceinline__ float largest(const f32x16 &s)
 
 // O^T += V^T P^T for 32 keys; the largest of the next scores is found beside
 // it (BESIDE).
-template <int VT, int DP, bool BESIDE>
+template <int VT, int DP, bool BESIDE, typename Loads>
 __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2], const char *values,
-                                           Ready<DP> ready, const f32x16 &next, float &top)
+                                           Ready<DP> ready, const f32x16 &next, float &top, Loads loads)
 {
     constexpr int kDims = Tiles<DP>::kDims, kN = 2 * kDims, kAhead = Ready<DP>::kN;
     const ValueReads<DP> read(values);
@@ -608,6 +636,7 @@ __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2], con
 #pragma unroll
             for (int i = n * 8 / kN; i < (n + 1) * 8 / kN; ++i) top = larger(top, next, 2 * i);
         }
+        loads(n, kN);
         in_order();
     }
 }
@@ -652,6 +681,8 @@ struct Parts {
     int64_t rows;         // n_tokens * n_q_heads
 };
 
+template <int N> using Const = std::integral_constant<int, N>;
+
 // The keys [from, to) of a tile by waves that own 32 rows each and share the
 // keys in WAYS ways: way y takes keys from + 64 (WAYS t + y) in turn t.
 //
@@ -660,160 +691,208 @@ struct Parts {
 // add its values, it finds the next maximum.  Keys are therefore wanted half a
 // turn before their values, and the key tiles in LDS lie half a turn ahead.
 // Two buffers each; a turn's reads run for the whole turn before it.
-template <int DT, int CDT, int DP, int WAYS>
-__device__ __forceinline__ void walk_rows(const AttnParams &p, const Plan &w, int kv_head, int group,
-                                          int wave, int from, int to, int lo, int hi, float c,
-                                          const u32x4 (&q)[Tiles<DP>::kSteps], char *lds, int *bad,
-                                          Rows<DP> &r)
-{
+template <int DT, int CDT, int DP, bool EXACT, int WAYS>
+struct RowWalk {
     using L = Tiles<DP>;
-    constexpr int VT = Types<DT, CDT>::V, kWaves = L::kWaves / WAYS;
-    constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf, kStride = 64 * WAYS;
-    using Keys = Stage<DT, CDT, DP, kWaves, true>;
-    using Vals = Stage<DT, CDT, DP, kWaves, false>;
-    const int way = wave / kWaves, first = from + way * 64;
-    lds += way * 4 * kTile;
-    const uint32_t at = lds_address(lds);
-    Keys sk(p, w, kv_head, wave % kWaves, first - kStride, kStride, from, to);   // tile t + 1: after turn t
-    Vals sv(p, w, kv_head, wave % kWaves, first, kStride, from, to);
+    static constexpr int VT = Types<DT, CDT>::V, kWaves = L::kWaves / WAYS;
+    static constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf, kStride = 64 * WAYS;
+    using Keys = Stage<DT, CDT, DP, EXACT, kWaves, true>;
+    using Vals = Stage<DT, CDT, DP, EXACT, kWaves, false>;
 
-    // limits of all of the wave's rows (they grow with the row), and of the tile's
-    const int wave_lo = __builtin_amdgcn_readlane(lo, 0);
-    const int wave_hi = min(__builtin_amdgcn_readlane(hi, 31), to);
-    const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
-    const int plain_hi = min(__builtin_amdgcn_readlane(hi, 0), to) - 32;
-    // keys that every row of the tile sees; elsewhere values are looked at
-    int blo, bhi, unused;
-    row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
-    row_limits(p, w, w.row0, group, unused, bhi);
-    bhi = min(bhi, to);
+    const AttnParams &p;
+    const Plan &w;
+    const int from, to, first;
+    char *lds;
+    const uint32_t at;
+    Keys sk;                          // its tile t + 1: what follows the first half of turn t
+    Vals sv;
 
-    const int n_turns = (to - from + kStride - 1) / kStride;
-    const auto sees = [&](int t) {
-        const int key0 = first + t * kStride;
-        return t >= 0 && t < n_turns && key0 < wave_hi && key0 + 64 > wave_lo;
-    };
-    const auto hidden = [&](int key0, uint32_t there, f32x16 &y) {
-        if (key0 >= plain_lo && key0 <= plain_hi && there == 3) return;
-        hide(y, lo - key0, min(hi, to) - key0, there);
-    };
-    const auto read_keys = [&](int t) {       // the second half of turn t, the first of t + 1
-        if ((t + 1) % Keys::kBatch == 0) sk.find_pages(t + 1);
-        sk.template fetch<false>(t + 1, at + ((t + 1) & 1) * kTile);
-    };
+    __device__ RowWalk(const AttnParams &p, const Plan &w, int kv_head, int wave, int from, int to, char *lds)
+        : p(p), w(w), from(from), to(to), first(from + wave / kWaves * 64),
+          lds(lds + wave / kWaves * 4 * kTile), at(lds_address(this->lds)),
+          sk(p, w, kv_head, wave % kWaves, first - kStride, kStride, from, to),
+          sv(p, w, kv_head, wave % kWaves, first, kStride, from, to)
+    {
+        sk.find_pages(0);
+        sv.find_pages(0);
+        sk.template fetch<false>(0, at);
+    }
 
-    f32x16 a = 0.0f, b = 0.0f;                // scores of a turn's halves
-    u32x4 x[2];
-    float top = -INFINITY, none = 0.0f;
-    uint32_t next_there = 0;                  // groups of the next turn that are on a page
-    if (n_turns > 0) read_keys(-1);
-    for (int t = -1; t < n_turns; ++t) {
-        char *keys = lds + ((t + 1) & 1) * kTile, *values = lds + (2 + (t & 1)) * kTile;
-        const int key0 = first + t * kStride;
-        const uint32_t there = next_there;
-        if constexpr (Keys::kDirect) {
-            wait_loads<0>();
-        } else {
-            sk.template store<false>(keys);
-            if (t >= 0) sv.template store<true>(values);
-        }
-        if (t >= 0 && (key0 < blo || key0 + 64 > bhi || there != 15))
-            sv.clean_values(values, t, there, bad);
-        __syncthreads();
-        // every wave is done with the last turn's buffers
-        if (t + 1 < n_turns) {
-            if ((t + 1) % Vals::kBatch == 0) sv.find_pages(t + 1);
+    // lo, hi: the limits of this lane's row.
+    __device__ __forceinline__ void run(int group, int lo, int hi, float c,
+                                        const u32x4 (&q)[Tiles<DP>::kSteps], int *bad, Rows<DP> &r)
+    {
+        // limits of all of the wave's rows (they grow with the row), and of the tile's
+        const int wave_hi = min(__builtin_amdgcn_readlane(hi, 31), to);
+        const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
+        const int plain_hi = min(__builtin_amdgcn_readlane(hi, 0), to) - 32;
+        // keys that every row of the tile sees; elsewhere values are looked at
+        int blo, bhi, unused;
+        row_limits(p, w, w.row0 + w.rows - 1, group, blo, unused);
+        row_limits(p, w, w.row0, group, unused, bhi);
+        bhi = min(bhi, to);
+        hi = min(hi, to);
+
+        const int n_turns = (to - from + kStride - 1) / kStride;
+        const auto part_hidden = [&](int key0, uint32_t there) {
+            return key0 < plain_lo || key0 > plain_hi || (there & 3) != 3;
+        };
+
+        f32x16 a, b;                          // scores of a turn's halves
+        u32x4 x[2];
+        float top, none = 0.0f;
+        uint32_t there = 0, next_there = sv.groups_there(0);   // groups on a page, of this turn and the next
+        // Begins turn t: its keys and values are there, every wave is done
+        // with the last turn's buffers, and the next turn's values and the
+        // keys after them may be read.  The last turn reads what nobody wants,
+        // from page 0.
+        const char *next_keys, *next_values;
+        uint32_t keys_at, values_at;
+        const auto begin = [&](int t, char *keys, char *values) {
+            if constexpr (Keys::kDirect) {
+                wait_loads<0>();
+            } else {
+                sk.template store<false>(keys);
+                if (t >= 0) sv.template store<true>(values);
+            }
+            const int key0 = first + t * kStride;
+            if (t >= 0 && (key0 < blo || key0 + 64 > bhi || there != 15))
+                sv.clean_values(values, t, there, bad);
+            __syncthreads();
+            if ((t + 1) % Vals::kBatch == 0 && t >= 0) sv.find_pages(t + 1);
+            if ((t + 2) % Keys::kBatch == 0) sk.find_pages(t + 2);
             next_there = sv.groups_there(t + 1);
-            sv.template fetch<true>(t + 1, at + (2 + ((t + 1) & 1)) * kTile);
-            read_keys(t + 1);
-        }
-        const bool more = sees(t + 1);
-        if (sees(t)) {
-            float base = move_top<DP>(r, both_halves(top), c);
-            scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, base);
+            next_values = sv.group_at(p.paged.v_cache, t + 1, 0);
+            next_keys = sk.group_at(p.paged.k_cache, t + 2, 0);
+            keys_at = at + (t & 1) * kTile;
+            values_at = at + (2 + ((t + 1) & 1)) * kTile;
+        };
+        const auto load = [&](int i) {        // of 2 kSlots
+            if (i % 2 == 0) sv.template fetch_part<true>(next_values, 0, i / 2, values_at);
+            else sk.template fetch_part<false>(next_keys, 0, i / 2, keys_at);
+        };
+        // The loads are spread over a turn: a CU's address unit takes 16
+        // cycles for each, and a wave that meets it busy waits.
+        const auto quarter = [&](auto which) {
+            return [&](int n, int of) {
+                constexpr int kLo = decltype(which)::value * 2 * Vals::kSlots / 4;
+                constexpr int kHi = (decltype(which)::value + 1) * 2 * Vals::kSlots / 4;
+#pragma unroll
+                for (int i = kLo; i < kHi; ++i)
+                    if ((i - kLo) * of / (kHi > kLo ? kHi - kLo : 1) == n) load(i);
+            };
+        };
+        const auto all_loads = [&] {
+#pragma unroll
+            for (int i = 0; i < 2 * Vals::kSlots; ++i) load(i);
+        };
+
+        begin(-1, lds, lds);                  // brings the first 32 keys
+        all_loads();
+        scores<DT, VT, DP, false>(a, q, lds + kHalf, b, x, none, c, 0.0f, NoLoads{});
+        hide(a, lo - first, hi - first, next_there);
+        top = largest(a);
+        for (int t = 0; t < n_turns; ++t) {
+            char *keys = lds + ((t + 1) & 1) * kTile, *values = lds + (2 + (t & 1)) * kTile;
+            const int key0 = first + t * kStride;
+            there = next_there;
+            begin(t, keys, values);
+            if (key0 >= wave_hi) {            // past what the wave's rows see
+                all_loads();
+                continue;
+            }
+            const bool hide_b = part_hidden(key0 + 32, there >> 2);
+            const bool hide_a = part_hidden(key0 + kStride, next_there);
+            move_top<DP>(r, top, c);
+            scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, r.base, quarter(Const<0>{}));
             Ready<DP> ready = read_ahead<DP>(values);
-            hidden(key0 + 32, there >> 2, b);
+            if (hide_b) hide(b, lo - key0 - 32, hi - key0 - 32, there >> 2);
             in_order();
-            add_values<VT, DP, true>(r, x, values, ready, b, top);
-            base = move_top<DP>(r, both_halves(top), c);
+            add_values<VT, DP, true>(r, x, values, ready, b, top, quarter(Const<1>{}));
+            move_top<DP>(r, top, c);
             // in the last turn the next scores are of keys that nobody wants,
             // and so is their maximum
-            scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, base);
+            scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, r.base, quarter(Const<2>{}));
             ready = read_ahead<DP>(values + kHalf);
-            if (more) hidden(key0 + kStride, next_there & 3, a);
+            if (hide_a) hide(a, lo - key0 - kStride, hi - key0 - kStride, next_there);
             in_order();
-            add_values<VT, DP, true>(r, x, values + kHalf, ready, a, top);
-        } else if (more) {
-            scores<DT, VT, DP, false>(a, q, keys + kHalf, b, x, none, c, 0.0f);
-            hidden(key0 + kStride, next_there & 3, a);
-            top = largest(a);
+            add_values<VT, DP, true>(r, x, values + kHalf, ready, a, top, quarter(Const<3>{}));
         }
+        wait_loads<0>();                      // before anyone else uses the buffers
     }
-}
+};
 
 // The keys [from, to) of a tile whose rows every wave has: a wave takes every
 // kWaves-th 32 keys.  It has a buffer of its own: the next keys are read once
 // the scores are done with these, the next values once O is.
-template <int DT, int CDT, int DP>
-__device__ __forceinline__ void walk_keys(const AttnParams &p, const Plan &w, int kv_head, int wave,
-                                          int from, int to, int lo, int hi, float c,
-                                          const u32x4 (&q)[Tiles<DP>::kSteps], char *lds, int *bad,
-                                          Rows<DP> &r)
-{
+template <int DT, int CDT, int DP, bool EXACT>
+struct KeyWalk {
     using L = Tiles<DP>;
-    using S = Stage<DT, CDT, DP, 1, false>;
-    constexpr int VT = Types<DT, CDT>::V;
-    constexpr int kStep = 32 * L::kWaves, kHalf = 32 * L::kRow;
-    const int first = from + wave * 32;
-    S st(p, w, kv_head, 0, first, kStep, from, to);
-    char *keys = lds + wave * 2 * kHalf, *values = keys + kHalf;
-    const uint32_t keys_at = lds_address(keys), values_at = keys_at + kHalf;
-    const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
-    const int plain_hi = min(__builtin_amdgcn_readlane(hi, 0), to) - 32;
-    const int n_tiles = to > first ? (to - first + kStep - 1) / kStep : 0;
-    if (n_tiles > 0) {
-        st.find_pages(0);
-        st.template fetch<false>(0, keys_at);
-        st.template fetch<true>(0, values_at);
-    }
-    for (int t = 0; t < n_tiles; ++t) {
-        const int key0 = first + t * kStep;
-        const bool more = t + 1 < n_tiles;
-        const uint32_t there = st.groups_there(t);
-        f32x16 s;
-        u32x4 x[2];
-        float unused;
-        if constexpr (S::kDirect) {
-            wait_loads<S::kLoads>();                 // the values may be on their way
-        } else {
-            st.template store<false>(keys);
-            st.template store<true>(values);
-        }
-        scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f);
-        if (more) {
-            if ((t + 1) % S::kBatch == 0) st.find_pages(t + 1);
-            wait_lds();
-            st.template fetch<false>(t + 1, keys_at);
-            if constexpr (!S::kDirect) st.template fetch<true>(t + 1, values_at);
-        }
-        const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
-        if (!whole) hide(s, lo - key0, min(hi, to) - key0, there);
-        const float base = move_top<DP>(r, both_halves(largest(s)), c);
-        exponentials<VT>(s, x, r.sum, c, base, 0, 16);
-        if constexpr (S::kDirect) {
-            if (more) wait_loads<S::kLoads>();
-            else wait_loads<0>();
-        }
-        if (!whole) st.clean_values(values, t, there, bad);
-        add_values<VT, DP, false>(r, x, values, read_ahead<DP>(values), s, unused);
-        if constexpr (S::kDirect) {
-            wait_lds();
-            if (more) st.template fetch<true>(t + 1, values_at);
-        }
-    }
-}
+    using S = Stage<DT, CDT, DP, EXACT, 1, false>;
+    static constexpr int VT = Types<DT, CDT>::V;
+    static constexpr int kStep = 32 * L::kWaves, kHalf = 32 * L::kRow;
 
-template <int DT, int CDT, int DP>
+    const int to, first, n_tiles;
+    char *keys;
+    const uint32_t at;
+    S st;
+
+    __device__ KeyWalk(const AttnParams &p, const Plan &w, int kv_head, int wave, int from, int to, char *lds)
+        : to(to), first(from + wave * 32), n_tiles(to > first ? (to - first + kStep - 1) / kStep : 0),
+          keys(lds + wave * 2 * kHalf), at(lds_address(keys)), st(p, w, kv_head, 0, first, kStep, from, to)
+    {
+        if (n_tiles == 0) return;
+        st.find_pages(0);
+        st.template fetch<false>(0, at);
+        st.template fetch<true>(0, at + kHalf);
+    }
+
+    __device__ __forceinline__ void run(int lo, int hi, float c, const u32x4 (&q)[Tiles<DP>::kSteps],
+                                        int *bad, Rows<DP> &r)
+    {
+        char *values = keys + kHalf;
+        hi = min(hi, to);
+        const int plain_lo = __builtin_amdgcn_readlane(lo, 31);
+        const int plain_hi = __builtin_amdgcn_readlane(hi, 0) - 32;
+        for (int t = 0; t < n_tiles; ++t) {
+            const int key0 = first + t * kStep;
+            const bool more = t + 1 < n_tiles;
+            const uint32_t there = st.groups_there(t);
+            f32x16 s;
+            u32x4 x[2];
+            float unused;
+            if constexpr (S::kDirect) {
+                wait_loads<S::kLoads>();             // the values may be on their way
+            } else {
+                st.template store<false>(keys);
+                st.template store<true>(values);
+            }
+            scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f, NoLoads{});
+            if (more) {
+                if ((t + 1) % S::kBatch == 0) st.find_pages(t + 1);
+                wait_lds();
+                st.template fetch<false>(t + 1, at);
+                if constexpr (!S::kDirect) st.template fetch<true>(t + 1, at + kHalf);
+            }
+            const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
+            if (!whole) hide(s, lo - key0, hi - key0, there);
+            move_top<DP>(r, largest(s), c);
+            exponentials<VT>(s, x, r.sum, c, r.base, 0, 16);
+            if constexpr (S::kDirect) {
+                if (more) wait_loads<S::kLoads>();
+                else wait_loads<0>();
+            }
+            if (!whole) st.clean_values(values, t, there, bad);
+            add_values<VT, DP, false>(r, x, values, read_ahead<DP>(values), s, unused, NoLoads{});
+            if constexpr (S::kDirect) {
+                wait_lds();
+                if (more) st.template fetch<true>(t + 1, at + kHalf);
+            }
+        }
+    }
+};
+
+template <int DT, int CDT, int DP, bool EXACT>
 __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void attend(
     AttnParams p, Parts parts, int tiles, int tile_rows, int max_splits)
 {
@@ -823,6 +902,7 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
     __shared__ __attribute__((aligned(16))) char lds[L::kLds];
     __shared__ int bad;          // a hidden place may hold a value that is not finite
     __shared__ float wave_stats[kWaves][32][2];
+    __shared__ int64_t wave_rows[kWaves][32][2];
 
     const PagedParams &g = p.paged;
     const int lane = int(threadIdx.x) & (kLanes - 1);
@@ -846,41 +926,48 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
                      : (kWaves == 8 && w.rows <= 4 * kRowsPerWave ? 2 : 1);
     const int row_waves = kWaves / ways;
 
-    // this lane's row, its limits, and its queries (rows past the last repeat it)
+    // this lane's row and its limits (rows past the last repeat it)
     const int first = wave % row_waves * kRowsPerWave;
     const int row = w.row0 + min(first + col, w.rows - 1);
     const int token = w.begin + row / group, head = kv_head * group + row % group;
     int lo, hi;
     row_limits(p, w, row, group, lo, hi);
+    const T *src = static_cast<const T *>(p.q) + int64_t(token) * p.q_stride +
+                   int64_t(head) * p.head_dim + half * 8;
+    // its place among the outputs, for the way out
+    if (half == 0) {
+        wave_rows[wave][col][0] = int64_t(token) * p.out_stride + int64_t(head) * p.head_dim;
+        wave_rows[wave][col][1] = split * parts.rows + int64_t(token) * p.n_q_heads + head;
+    }
+    const float c = p.scale * g.k_scale * kLog2e;
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+
     u32x4 q[L::kSteps];
-    {
-        const T *src = static_cast<const T *>(p.q) + int64_t(token) * p.q_stride +
-                       int64_t(head) * p.head_dim + half * 8;
+    const auto read_queries = [&] {
 #pragma unroll
         for (int st = 0; st < L::kSteps; ++st)
-            q[st] = st * 16 < p.head_dim ? *reinterpret_cast<const u32x4 *>(src + st * 16) : u32x4(0u);
+            q[st] = EXACT || st * 16 < p.head_dim ? *reinterpret_cast<const u32x4 *>(src + st * 16) : u32x4(0u);
         // wait for them here: a wait inside the loop would be one for the next
         // tile's reads as well
 #pragma unroll
         for (int st = 0; st < L::kSteps; ++st) asm volatile("" : "+v"(q[st]));
-    }
-    const float c = p.scale * g.k_scale * kLog2e;
-
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
+    };
     Rows<DP> r;
-    r.top = -INFINITY;
-    r.sum = 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < L::kDims; ++dt) r.o[dt] = 0.0f;
-
-    if (ways == 1)
-        walk_rows<DT, CDT, DP, 1>(p, w, kv_head, group, wave, from, to, lo, hi, c, q, lds, &bad, r);
-    else if (ways == 2)
-        walk_rows<DT, CDT, DP, kWaves == 8 ? 2 : 1>(p, w, kv_head, group, wave, from, to, lo, hi, c, q,
-                                                    lds, &bad, r);
-    else
-        walk_keys<DT, CDT, DP>(p, w, kv_head, wave, from, to, lo, hi, c, q, lds, &bad, r);
+    // each walk begins its first reads when it is made; the queries come beside them
+    if (ways == 1) {
+        RowWalk<DT, CDT, DP, EXACT, 1> walk(p, w, kv_head, wave, from, to, lds);
+        read_queries();
+        walk.run(group, lo, hi, c, q, &bad, r);
+    } else if (ways == 2) {
+        RowWalk<DT, CDT, DP, EXACT, kWaves == 8 ? 2 : 1> walk(p, w, kv_head, wave, from, to, lds);
+        read_queries();
+        walk.run(group, lo, hi, c, q, &bad, r);
+    } else {
+        KeyWalk<DT, CDT, DP, EXACT> walk(p, w, kv_head, wave, from, to, lds);
+        read_queries();
+        walk.run(lo, hi, c, q, &bad, r);
+    }
     r.sum += __shfl_xor(r.sum, 32);
 
     // Every wave's O goes through LDS, so that stores are whole rows; waves
@@ -913,34 +1000,38 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
             }
     }
     __syncthreads();
-    const int fours = p.head_dim / 4;
-    for (int i = int(threadIdx.x); i < w.rows * fours; i += kWaves * kLanes) {
-        const int n = i / fours, d = (i - n * fours) * 4;
-        f32x4 x = 0.0f;
-        float top = -INFINITY, sum = 0.0f;
-        for (int k = n / 32; k < kWaves; k += row_waves) {
-            x += *reinterpret_cast<const f32x4 *>(all + (k * 32 + n % 32) * kRow + d);
-            top = fmaxf(top, wave_stats[k][n % 32][0]);
+    // four dims a lane, a row to 32 or 64 lanes
+    constexpr int kRowLanes = DP <= 128 ? 32 : 64, kRowsAtOnce = kWaves * kLanes / kRowLanes;
+    const int d = int(threadIdx.x) % kRowLanes * 4;
+    const bool look = bad != 0;
+    for (int n = int(threadIdx.x) / kRowLanes; n < w.rows; n += kRowsAtOnce) {
+        if (d >= p.head_dim) continue;
+        const int k0 = n / 32, col = n % 32;
+        f32x4 x = *reinterpret_cast<const f32x4 *>(all + n * kRow + d);
+        float top = wave_stats[k0][col][0], sum = wave_stats[k0][col][1];
+        if (ways > 1) {
+            const float own = top;
+            for (int k = k0 + row_waves; k < kWaves; k += row_waves) {
+                x += *reinterpret_cast<const f32x4 *>(all + (k * 32 + col) * kRow + d);
+                top = fmaxf(top, wave_stats[k][col][0]);
+            }
+            sum = sum == 0.0f ? 0.0f : sum * weight(own, top);
+            for (int k = k0 + row_waves; k < kWaves; k += row_waves) {
+                const float part = wave_stats[k][col][1];
+                if (part != 0.0f) sum += part * weight(wave_stats[k][col][0], top);
+            }
         }
-        for (int k = n / 32; k < kWaves; k += row_waves) {
-            const float part = wave_stats[k][n % 32][1];
-            if (ways == 1) sum = part;
-            else if (part != 0.0f) sum += part * weight(wave_stats[k][n % 32][0], top);
-        }
-        const int row = w.row0 + n;
-        const int64_t t = w.begin + row / group;
-        const int h = kv_head * group + row % group;
-        if (bad) {
+        if (look) {
             int lo, hi;
-            row_limits(p, w, row, group, lo, hi);
+            row_limits(p, w, w.row0 + n, group, lo, hi);
             x += non_finite_sum<CDT>(p, g.block_table + int64_t(w.seq) * g.max_pages, kv_head, d,
                                      max(lo, from), min(hi, to));
         }
         if (w.splits == 1) {
             x *= sum == 0.0f ? 0.0f : g.v_scale / sum;
-            store4<DT>(static_cast<T *>(p.out) + t * p.out_stride + int64_t(h) * p.head_dim + d, x);
+            store4<DT>(static_cast<T *>(p.out) + wave_rows[k0][col][0] + d, x);
         } else {
-            const int64_t part = split * parts.rows + t * p.n_q_heads + h;
+            const int64_t part = wave_rows[k0][col][1];
             *reinterpret_cast<f32x4 *>(parts.o + part * p.head_dim + d) = x;
             if (d == 0) parts.stats[part] = make_float2(top * c, sum);
         }
@@ -1070,25 +1161,28 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
 
 size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
 
-template <int DT, int CDT, int DP>
+template <int DT, int CDT, int DP, bool EXACT>
 void launch(const AttnParams &p, const Parts &parts, const Shape &s, hipStream_t stream)
 {
     const dim3 grid(uint32_t(s.tiles * p.n_k_heads), uint32_t(s.splits));
-    attend<DT, CDT, DP><<<grid, Tiles<DP>::kWaves * kLanes, 0, stream>>>(p, parts, int(s.tiles),
-                                                                         s.tile_rows, s.splits);
+    attend<DT, CDT, DP, EXACT><<<grid, Tiles<DP>::kWaves * kLanes, 0, stream>>>(
+        p, parts, int(s.tiles), s.tile_rows, s.splits);
 }
 
+// Common widths have kernels of their own; the others take the next of three,
+// with zeros behind the head.
 template <int DT, int CDT>
 void launch_attend(const AttnParams &p, const Parts &parts, const Shape &s, hipStream_t stream)
 {
     const int d = p.head_dim;
-    if (d <= 32) launch<DT, CDT, 32>(p, parts, s, stream);
-    else if (d <= 64) launch<DT, CDT, 64>(p, parts, s, stream);
-    else if (d <= 80) launch<DT, CDT, 80>(p, parts, s, stream);
-    else if (d <= 96) launch<DT, CDT, 96>(p, parts, s, stream);
-    else if (d <= 128) launch<DT, CDT, 128>(p, parts, s, stream);
-    else if (d <= 192) launch<DT, CDT, 192>(p, parts, s, stream);
-    else launch<DT, CDT, 256>(p, parts, s, stream);
+    if (d == 64) launch<DT, CDT, 64, true>(p, parts, s, stream);
+    else if (d == 80) launch<DT, CDT, 80, true>(p, parts, s, stream);
+    else if (d == 96) launch<DT, CDT, 96, true>(p, parts, s, stream);
+    else if (d == 128) launch<DT, CDT, 128, true>(p, parts, s, stream);
+    else if (d == 256) launch<DT, CDT, 256, true>(p, parts, s, stream);
+    else if (d < 64) launch<DT, CDT, 64, false>(p, parts, s, stream);
+    else if (d < 128) launch<DT, CDT, 128, false>(p, parts, s, stream);
+    else launch<DT, CDT, 256, false>(p, parts, s, stream);
 }
 
 }  // namespace

@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kRowsPerWave = 32;
 constexpr int kUnit = 256;            // keys: ranges of a split are multiples of this
-constexpr int kMinUnits = 1;          // and at least this many
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -121,7 +120,7 @@ __device__ __forceinline__ void plan_keys(const AttnParams &p, Plan &w, int grou
     w.hi = hi > w.lo ? hi : w.lo;
     const int units = (w.hi - w.lo + kUnit - 1) / kUnit;
     int per = (units + max_splits - 1) / max_splits;
-    per = per < kMinUnits ? kMinUnits : per;
+    per = per < 1 ? 1 : per;
     w.per = per * kUnit;
     w.splits = units > per ? (units + per - 1) / per : 1;
 }
@@ -1124,36 +1123,36 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
 {
     const int64_t group = n_q_heads / n_k_heads, rows = n_tokens * group;
     const int64_t slots = 256;           // blocks the chip holds: one for each CU
-    Shape s;
-    s.tile_rows = head_dim <= 128 && rows / 256 * n_k_heads >= 2 * slots ? 256 : 128;
-    s.tiles = rows / s.tile_rows + n_seqs;
-    const int64_t blocks = s.tiles * n_k_heads;
     const int64_t units = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
-    s.splits = 1;
-    if (blocks == 0 || units <= 2) return s;
+    Shape s = {128, rows / 128 + n_seqs, 1};
     if (rows <= int64_t(n_seqs) * kRowsPerWave) {
-        // few rows: the keys are read once and HBM decides.  Enough blocks to
-        // fill the chip, and then more while each still has 4 units, so that
-        // sequences of different lengths end together
-        int64_t n = slots / blocks;
-        if (n > units) n = units;
-        int64_t fine = 2048 / blocks;
-        if (fine * 4 > units) fine = units / 4;
-        n = n > fine ? n : fine;
-        n = n < 256 ? n : 256;
+        // Few rows: the keys are read once and HBM decides, so the chip is
+        // filled once.  Two sequences of 262144 keys, 4 heads, e4m3: 32 splits
+        // 54 us, 16 66, 64 60, 128 73.  A join costs as much as 8 units: one
+        // sequence, 8 heads, of 2048 keys 13.3 us whole and 13.8 split, of
+        // 4096 24 and 16.
+        const int64_t blocks = s.tiles * n_k_heads;
+        if (blocks == 0 || units <= 8) return s;
+        const int64_t n = slots / blocks < units ? slots / blocks : units;
         s.splits = int(n < 1 ? 1 : n);
         return s;
     }
-    // many rows: the blocks run in rounds of `slots`; a split costs about two
-    // units more in each block and, where there are any, four for the join
-    const int64_t full = (rows + (n_seqs - 1) * (s.tile_rows / 2) + s.tile_rows - 1) / s.tile_rows *
-                         n_k_heads;                        // about the tiles that have rows
+    // Many rows: the blocks run in rounds of `slots`.  In units' times of 128
+    // rows, a block takes one or (256 rows, no waves that share keys) two for
+    // each unit, 6 or 8 to begin and end, and the join one.  128 rows against
+    // 256, the first by the rule's choice: 288 blocks of 2688 keys 90 us and
+    // 78, 1152 of 8192 755 and 710, 228 of 16384 74 and 104; 16 blocks of 8192
+    // keys whole 131 us, in 16 splits 37.
     int64_t best = INT64_MAX;
-    for (int n = 1; n <= 8 && n * kMinUnits <= units; ++n) {
-        const int64_t cost = (full * n + slots - 1) / slots * ((units + n - 1) / n + 2) + (n > 1 ? 4 : 0);
-        if (cost < best) {
+    for (int tile_rows = 128; tile_rows <= (head_dim <= 128 ? 256 : 128); tile_rows *= 2) {
+        const int64_t full = (rows + int64_t(n_seqs - 1) * (tile_rows / 2) + tile_rows - 1) / tile_rows *
+                             n_k_heads;                    // about the tiles that have rows
+        for (int n = 1; n <= 16 && n <= units; ++n) {
+            const int64_t block = (units + n - 1) / n * (tile_rows / 128) + 4 + tile_rows / 64;
+            const int64_t cost = (full * n + slots - 1) / slots * block + (n > 1);
+            if (cost >= best) continue;
             best = cost;
-            s.splits = n;
+            s = {tile_rows, rows / tile_rows + n_seqs, n};
         }
     }
     return s;
@@ -1214,7 +1213,11 @@ hipError_t run_paged_attention(const AttnParams &p, hipStream_t stream)
     else launch_attend<kBF16, kE4M3>(p, parts, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1) return e;
-    const dim3 blocks(uint32_t(s.tiles * p.n_k_heads), s.splits >= 16 ? 8 : 1);
+    // 16 rows a block; tiles of few rows and few splits are done by one (320
+    // tiles, 2 splits: 241 us against 249)
+    const bool few = parts.rows <= int64_t(p.paged.n_seqs) * p.n_k_heads * kRowsPerWave;
+    const dim3 blocks(uint32_t(s.tiles * p.n_k_heads),
+                      few && s.splits < 16 ? 1 : uint32_t(s.tile_rows / 16));
     if (p.dtype == kF16) attend_join<kF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.tile_rows, s.splits);
     else attend_join<kBF16><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.tile_rows, s.splits);
     return hipGetLastError();

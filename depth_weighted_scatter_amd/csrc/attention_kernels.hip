@@ -292,7 +292,12 @@ struct Stage {
     int row_bytes;
     uint32_t group_lo, group_hi;               // lane's group: its byte offset in the cache
     uint64_t have;                             // groups that are on a page
-    int offset[2][kSlots];                     // lane's pieces: bytes from their group, -1 for a zero
+    // Where rows have a power of two of pieces, the swizzle of a later load is
+    // that of the first with some bits turned: registers for all of them would
+    // spill in wide heads, and each reload waits for the reads in flight (2 x 1024
+    // tokens over 4096 keys, 16 heads of 256 on 4, bf16: 348 -> 269 us).
+    static constexpr bool kOne = EXACT && kHalves == 1 && L::kRound == L::kPieces;
+    int offset[2][kOne ? 1 : kSlots];          // lane's pieces: bytes from their group, -1 for a zero
     u32x2 k[kDirect ? 1 : kLoads], v[kDirect ? 1 : kLoads];
 
     __device__ Stage(const AttnParams &p, const Plan &w, int kv_head, int wave, int first,
@@ -302,7 +307,7 @@ struct Stage {
           row_bytes(p.head_dim * int(sizeof(C)))
     {
 #pragma unroll
-        for (int n = 0; n < kSlots; ++n) {
+        for (int n = 0; n < (kOne ? 1 : kSlots); ++n) {
             const int id = part(n) * kLanes + (int(threadIdx.x) & (kLanes - 1));
             const int key = id / L::kPieces, at = id % L::kPieces;
 #pragma unroll
@@ -350,6 +355,17 @@ struct Stage {
         else return part(n) * kLanes + (int(threadIdx.x) & (kLanes - 1)) < 16 * L::kPieces;
     }
 
+    template <bool VALUES> __device__ __forceinline__ int offset_of(int n) const
+    {
+        if constexpr (kOne) {
+            const int key = n * kLanes / L::kPieces;
+            const int turned = VALUES ? L::value_swizzle(key) : L::key_swizzle(key);
+            return (offset[VALUES][0] ^ (turned * 8 * int(sizeof(C)))) + key * DP * int(sizeof(C));
+        } else {
+            return offset[VALUES][n];
+        }
+    }
+
     // Where the wave's i-th group of a tile lies in a cache.
     __device__ __forceinline__ const char *group_at(const void *cache, int tile, int i) const
     {
@@ -365,12 +381,15 @@ struct Stage {
     __device__ __forceinline__ void fetch_part(const char *base, int i, int n, uint32_t lds)
     {
         const uint32_t to = lds + (WAVES > 1 ? wave % 4 : i) * kGroupBytes + part(n) * 1024;
-        const int off = offset[VALUES][n];
+        const int off = offset_of<VALUES>(n);
         if constexpr (kDirect) {
             if (!has_piece(n)) return;
             if constexpr (EXACT) load_to_lds(base, uint32_t(off), to);
             else load_to_lds(off < 0 ? reinterpret_cast<const char *>(&kZeroPiece) : base + off, to);
         } else {
+            // in wide heads, an address made here: with the same load on two
+            // paths, the addresses of all would otherwise be kept, and spill
+            if constexpr (DP > 128) asm volatile("" : "+s"(base));
             u32x2 x = 0u;
             if (has_piece(n) && (EXACT || off >= 0)) x = *reinterpret_cast<const u32x2 *>(base + uint32_t(off));
             (VALUES ? v : k)[i * kSlots + n] = x;
@@ -948,9 +967,15 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
         for (int st = 0; st < L::kSteps; ++st)
             q[st] = EXACT || st * 16 < p.head_dim ? *reinterpret_cast<const u32x4 *>(src + st * 16) : u32x4(0u);
         // wait for them here: a wait inside the loop would be one for the next
-        // tile's reads as well
+        // tile's reads as well.  Wide heads of e4m3 caches, whose keys and
+        // values pass through registers, leave these no other place than the
+        // accumulators' side (with addresses made at each load: 766 -> 427 us for 2 x 1024
+        // tokens over 4096 keys, 16 heads on 4)
 #pragma unroll
-        for (int st = 0; st < L::kSteps; ++st) asm volatile("" : "+v"(q[st]));
+        for (int st = 0; st < L::kSteps; ++st) {
+            if constexpr (DP > 128 && CDT == kE4M3) asm volatile("" : "+a"(q[st]));
+            else asm volatile("" : "+v"(q[st]));
+        }
     };
     Rows<DP> r;
     // each walk begins its first reads when it is made; the queries come beside them

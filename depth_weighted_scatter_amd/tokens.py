@@ -60,6 +60,9 @@ def _lib():
     return _declare(_load())
 
 
+MAX_WINDOW = 2 ** 31 - 1             # past every place: as good as none
+
+
 # ---- the things a program keeps ------------------------------------------------------------
 @dataclasses.dataclass(frozen=True)
 class Rope:
@@ -453,8 +456,8 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
         "bevpool_paged_attention")
     rc = lib.bevpool_paged_attention(
         q.data_ptr(), sq, _TOKEN_DTYPE[q.dtype], n, hq, hk, dim, *paged,
-        dim ** -0.5 if scale is None else float(scale), int(causal), int(window), out.data_ptr(),
-        so, ws.data_ptr(), ws.numel(), _raw_stream(q))
+        dim ** -0.5 if scale is None else float(scale), int(causal),
+        min(max(int(window), -1), MAX_WINDOW), out.data_ptr(), so, ws.data_ptr(), ws.numel(), _raw_stream(q))
     if rc != OK:
         raise BevPoolError("bevpool_paged_attention", rc)
     return out

@@ -318,6 +318,122 @@ def test_attention_same_bits_and_overlapping_calls():
         assert all(torch.equal(g, want) for g in got)
 
 
+@pytest.mark.parametrize("dim,dtype,cache", [(64, "f16", "f16"), (80, "bf16", "e4m3"),
+                                             (96, "f16", "e4m3"), (128, "bf16", "bf16"),
+                                             (128, "f16", "e4m3"), (48, "bf16", "bf16"),
+                                             (112, "f16", "f16")])
+@pytest.mark.parametrize("mask", ["causal", "all", "window"])
+def test_attention_many_rows(dim, dtype, cache, mask):
+    """Enough rows for tiles of 256: 15616 a key head are 122 tiles of 128 or 61
+    of 256, for each of four key heads, on 256 CUs.  The last of a sequence is
+    not full.  Some heads of two key heads against the oracle."""
+    rng = np.random.default_rng(33)
+    new, ctx, hq, hk, page = [573, 3, 400], [95, 300, 41], 64, 4, 32
+    b = Batch(rng, new, ctx, hk, dim, page, dtype, cache)
+    q = values(rng, (b.n, hq, dim), dtype, 1.5)
+    causal, window = mask != "all", 150 if mask == "window" else 0
+    got = dws.bevpool_paged_attention(q[0], b.pool, b.batch, causal=causal, window=window)
+    torch.cuda.synchronize()
+    assert torch.isfinite(got).all()
+    for g, heads in ((2, slice(33, 48, 7)), (0, slice(0, 16, 15))):
+        # the heads picked share key head g, so the oracle gets that one alone
+        want, mag, spread, seen = ref.attention(q[1][:, heads], b.k0[:, g:g + 1], b.v0[:, g:g + 1],
+                                                b.offsets, b.kv, b.table, dim ** -0.5, causal, window)
+        u = U["f16" if cache == "e4m3" else dtype]
+        rel = (u + 4 * (dim + 8) * E32 * spread + 2.0 ** -20 + 2 * seen * E32 + 2.0 ** -20)[..., None]
+        err = mag * rel * (1 + U[dtype]) + U[dtype] * np.abs(want) + TINY[dtype]
+        if u == U["f16"]:
+            err = err + (seen * 2.0 ** -25)[..., None] * np.nanmax(np.abs(b.v0))
+        within(host(got[:, heads]), want, err, f"key head {g}")
+
+
+@pytest.mark.parametrize("dim,cache", [(128, "bf16"), (256, "bf16"), (256, "e4m3"), (64, "e4m3")])
+def test_attention_few_blocks_in_splits(dim, cache):
+    """Tiles of many rows whose keys are cut over blocks: those of a sequence
+    that ends early have no key in the later ones."""
+    rng = np.random.default_rng(34)
+    b = Batch(rng, [40, 90, 2], [4100, 30, 0], 2, dim, 64, "bf16", cache)
+    q = values(rng, (b.n, 6, dim), "bf16", 1.5)
+    _check_attention(b, q, 6)
+    _check_attention(b, q, 6, causal=False, window=2000)
+
+
+@pytest.mark.parametrize("new,ctx", [([1], [200]), ([48], [152]), ([200], [100])])
+def test_attention_hidden_nan_codes(new, ctx):
+    """The same of e4m3 caches, whose one value that is not finite is NaN."""
+    rng = np.random.default_rng(35)
+    b = Batch(rng, new, ctx, 1, 128, 16, "f16", "e4m3")
+    q = values(rng, (b.n, 2, 128), "f16")
+    kv, n = int(b.kv[0]), int(new[0])
+    page, slot, first = b.table[0, (kv - 1) // 16], (kv - 1) % 16, b.table[0, 0]
+    k, v = b.k0.copy(), b.v0.copy()
+    v[page, 0, slot, 5] = k[first, 0, 0, :] = v[first, 0, 0, :] = np.nan
+    _codes(b.vt)[page, 0, slot, 5] = 0x7f
+    _codes(b.kt)[first, 0, 0], _codes(b.vt)[first, 0, 0] = 0xff, 0x7f
+    got = _check_attention(b, q, 2, window=kv - n, k=k, v=v)
+    assert torch.isfinite(got[:-1]).all() and torch.isnan(got[-1, :, 5]).all()
+    assert torch.isfinite(got[-1, :, :5]).all() and torch.isfinite(got[-1, :, 6:]).all()
+
+
+def test_attention_graphs_that_share_a_workspace():
+    """Two graphs captured with one workspace, replayed in turn on one stream
+    with eager calls between them."""
+    rng = np.random.default_rng(36)
+    b = Batch(rng, [1, 40], [9000, 2000], 2, 64, 64, "bf16", "bf16")
+    q = [values(rng, (b.n, 4, 64), "bf16")[0] for _ in range(2)]
+    need = dws.bevpool_paged_attention_workspace_size(b.n, 2, 4, 2, 64, 64, b.table.shape[1])
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
+    want = [dws.bevpool_paged_attention(x, b.pool, b.batch) for x in q]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in q:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(dws.bevpool_paged_attention(x, b.pool, b.batch, workspace=ws))
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        eager = dws.bevpool_paged_attention(q[0], b.pool, b.batch, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+        assert torch.equal(eager, want[0])
+
+
+def test_attention_refusals():
+    rng = np.random.default_rng(37)
+    b = Batch(rng, [3, 40], [4, 9000], 2, 64, 16, "bf16", "bf16")
+    q = values(rng, (b.n, 4, 64), "bf16")[0]
+    call = dws.bevpool_paged_attention
+    with pytest.raises(TypeError):
+        call(q.cpu(), b.pool, b.batch)
+    with pytest.raises((TypeError, ValueError, dws.BevPoolError)):
+        call(q.float(), b.pool, b.batch)                       # fp32 tokens
+    with pytest.raises((TypeError, ValueError, dws.BevPoolError)):
+        call(q.half(), b.pool, b.batch)                        # an fp16 query, a bf16 cache
+    with pytest.raises((ValueError, dws.BevPoolError)):
+        call(q[:, :3], b.pool, b.batch)                        # 3 heads on 2
+    with pytest.raises(ValueError):
+        call(q[:, :, :32], b.pool, b.batch)
+    with pytest.raises(ValueError):
+        call(q.transpose(0, 1), b.pool, b.batch)
+    with pytest.raises(dws.BevPoolError):
+        call(q, b.pool, b.batch, window=-1)
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises((ValueError, dws.BevPoolError)):
+            call(q, b.pool, b.batch, scale)
+    need = dws.bevpool_paged_attention_workspace_size(b.n, 2, 4, 2, 64, 16, b.table.shape[1])
+    with pytest.raises(dws.BevPoolError):
+        call(q, b.pool, b.batch, workspace=torch.empty(need - 256, dtype=torch.uint8, device=dev()))
+    with pytest.raises(TypeError):
+        call(q, b.pool, b.batch, workspace=torch.empty(need, device=dev()))
+    with pytest.raises(ValueError):
+        call(q, b.pool, b.batch, out=torch.empty_like(q)[:, :2])
+    with pytest.raises(ValueError):                            # a cache of another shape
+        dws.PagedCache(b.kt, b.vt[:1])
+
+
 # ---- in a row -----------------------------------------------------------------------------
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_frames_then_steps(cache):

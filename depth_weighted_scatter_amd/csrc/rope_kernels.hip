@@ -206,7 +206,10 @@ __global__ __launch_bounds__(kBlock) void norm_rope_fwd(RopeParams p, int chunk)
 
 // grid: (blocks over token groups, head chunks); a block walks over token
 // groups and leaves one partial row of the weight gradient.  A chunk never
-// holds both queries and keys.
+// holds both queries and keys.  Reading the next head before this one is worked
+// on costs the registers of a wave a SIMD and loses (16384 tokens of 16 + 4
+// heads of 128, forward and backward: 103 us against 101), and so does asking
+// for four waves (spills, 313 us).
 template <int DT, int LPR, bool ADJ>
 __global__ __launch_bounds__(kBlock) void norm_rope_bwd(RopeGradParams g, int chunk, int q_chunks)
 {
@@ -239,18 +242,17 @@ __global__ __launch_bounds__(kBlock) void norm_rope_bwd(RopeGradParams g, int ch
                 t * (is_q ? p.q_out_stride : p.k_out_stride);
         for (int h = h0; h < h1; ++h) {
             const int64_t row = int64_t(h) * p.head_dim;
-            f32x8 ga = 0.0f, gb = 0.0f;
+            f32x8 ga = 0.0f, gb = 0.0f, xa = 0.0f, xb = 0.0f;
             if (on) {
                 ga = load8<DT>(dy + row + s.a);
                 gb = load8<DT>(dy + row + s.b);
-            }
-            rotate<ADJ>(ga, gb, cs, -sn, s.pair >= 0);
-            if (weight) {
-                f32x8 xa = 0.0f, xb = 0.0f;
-                if (on) {
+                if (weight) {
                     xa = load8<DT>(x + row + s.a);
                     xb = load8<DT>(x + row + s.b);
                 }
+            }
+            rotate<ADJ>(ga, gb, cs, -sn, s.pair >= 0);
+            if (weight) {
                 const float ms = row_sum<LPR>(dot8(xa, xa) + dot8(xb, xb)) * inv_dim;
                 const float r = 1.0f / sqrtf(ms + p.eps);
                 xa *= r;
@@ -290,8 +292,11 @@ __global__ __launch_bounds__(kBlock) void norm_rope_bwd(RopeGradParams g, int ch
 }
 
 // Sums the partial rows: block (x, 0) the columns 16x.. of dq_weight, (x, 1)
-// of dk_weight.
-__global__ __launch_bounds__(kBlock) void sum_partials(const float *partials, int head_dim,
+// of dk_weight.  Some hundred rows that wait for memory: 64 strips a block,
+// eight loads of each at once (16 strips, one by one: 16 us of the call).
+constexpr int kSumBlock = 1024, kStrips = kSumBlock / 16;
+
+__global__ __launch_bounds__(kSumBlock) void sum_partials(const float *partials, int head_dim,
                                                        int q_rows, int k_rows, float *dq_weight,
                                                        float *dk_weight)
 {
@@ -302,12 +307,13 @@ __global__ __launch_bounds__(kBlock) void sum_partials(const float *partials, in
     const float *from = partials + (is_q ? 0 : int64_t(q_rows) * head_dim);
     const int col = int(blockIdx.x) * 16 + int(threadIdx.x) % 16, strip = int(threadIdx.x) / 16;
     float sum = 0.0f;
-    for (int r = strip; r < rows; r += 16) sum += from[int64_t(r) * head_dim + col];
-    __shared__ float part[16][16];
+#pragma unroll 8
+    for (int r = strip; r < rows; r += kStrips) sum += from[int64_t(r) * head_dim + col];
+    __shared__ float part[kStrips][16];
     part[strip][threadIdx.x % 16] = sum;
     __syncthreads();
     if (strip == 0) {
-        for (int i = 1; i < 16; ++i) sum += part[i][threadIdx.x % 16];
+        for (int i = 1; i < kStrips; ++i) sum += part[i][threadIdx.x % 16];
         out[col] = sum;
     }
 }
@@ -431,8 +437,12 @@ GradGrid grad_grid(int64_t n_tokens, int n_q_heads, int n_k_heads, int head_dim)
     g.chunk = head_chunk(blocks * kWavesPerBlock, n_q_heads + n_k_heads);
     g.q_chunks = (n_q_heads + g.chunk - 1) / g.chunk;
     g.k_chunks = (n_k_heads + g.chunk - 1) / g.chunk;
-    const int64_t most = 1024 / (g.q_chunks + g.k_chunks);
-    g.blocks = int(blocks < most ? blocks : (most > 1 ? most : 1));
+    // blocks the chip holds (2.5 for each CU, by their registers), with equal
+    // numbers of token groups: 16384 tokens of 16 + 4 heads of 128, forward and
+    // backward, 96 us with 640 or 768, 97 with 1280, 100 with 2560
+    const int64_t limit = 640 / (g.q_chunks + g.k_chunks), most = limit > 1 ? limit : 1;
+    const int64_t turns = (blocks + most - 1) / most;      // token groups a wave walks over
+    g.blocks = int(turns > 0 ? (blocks + turns - 1) / turns : 0);
     return g;
 }
 
@@ -495,7 +505,7 @@ hipError_t run_qk_norm_rope_backward(const RopeGradParams &g, hipStream_t stream
         if (e != hipSuccess) return e;
     }
     if (!p.q_weight && !p.k_weight) return hipSuccess;
-    sum_partials<<<dim3(uint32_t(p.head_dim / 16), 2), kBlock, 0, stream>>>(
+    sum_partials<<<dim3(uint32_t(p.head_dim / 16), 2), kSumBlock, 0, stream>>>(
         g.partials, p.head_dim, blocks * w.q_chunks, blocks * w.k_chunks,
         p.q_weight ? g.dq_weight : nullptr, p.k_weight ? g.dk_weight : nullptr);
     return hipGetLastError();

@@ -20,6 +20,17 @@
 // operand as they stand, and V^T is read from LDS in the same order by the
 // transposing read (four keys of one dim a lane), so the weights never leave
 // their registers.
+//
+// What bounds it.  Single tokens read each key and value once: 64 requests of
+// up to 8192 keys (32 heads on 8, 128 dims, bf16) 246 us, 5.6 TB/s; two of
+// 131072 (e4m3) 46 us and 7 for the join.  Chunks are bound by issue: for 64
+// keys of 128 dims a wave has 32 matrix instructions (1024 cycles of the
+// matrix cores), 32 exponentials and some 300 other instructions, and the two
+// waves of a SIMD take 4100 cycles for theirs.  4096 tokens after 8192 cached
+// ones (32 heads on 8) take 665 to 710 us, 1.0 PFLOP/s, at the clock that
+// power leaves; the library's large product reaches 1.18.  A block takes
+// about 14000 cycles to begin (its place, its queries, its first keys) and
+// 12000 to end; over 2816 keys (704 tokens, 80 dims: 77 us) that is a third.
 #include <hip/hip_runtime.h>
 
 #include "token_device.h"
@@ -1152,7 +1163,7 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
     Shape s = {128, rows / 128 + n_seqs, 1};
     if (rows <= int64_t(n_seqs) * kRowsPerWave) {
         // Few rows: the keys are read once and HBM decides, so the chip is
-        // filled once.  Two sequences of 262144 keys, 4 heads, e4m3: 32 splits
+        // filled once.  Two sequences of 131072 keys, 4 heads, e4m3: 32 splits
         // 54 us, 16 66, 64 60, 128 73.  A join costs as much as 8 units: one
         // sequence, 8 heads, of 2048 keys 13.3 us whole and 13.8 split, of
         // 4096 24 and 16.
@@ -1164,10 +1175,10 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
     }
     // Many rows: the blocks run in rounds of `slots`.  In units' times of 128
     // rows, a block takes one or (256 rows, no waves that share keys) two for
-    // each unit, 6 or 8 to begin and end, and the join one.  128 rows against
-    // 256, the first by the rule's choice: 288 blocks of 2688 keys 90 us and
-    // 78, 1152 of 8192 755 and 710, 228 of 16384 74 and 104; 16 blocks of 8192
-    // keys whole 131 us, in 16 splits 37.
+    // each unit, 6 or 8 to begin and end, and the join one.  Tiles of 128 rows
+    // against 256: 288 blocks of 2816 keys 90 us and 78, 1024 of up to 12288
+    // 755 and 710, 228 of up to 6333 74 and 104 (the rule takes the better in
+    // each); 16 blocks of 8192 keys 131 us whole and 37 in 16 splits.
     int64_t best = INT64_MAX;
     for (int tile_rows = 128; tile_rows <= (head_dim <= 128 ? 256 : 128); tile_rows *= 2) {
         const int64_t full = (rows + int64_t(n_seqs - 1) * (tile_rows / 2) + tile_rows - 1) / tile_rows *

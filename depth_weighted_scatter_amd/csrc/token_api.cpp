@@ -292,11 +292,11 @@ int bevpool_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_
 
 namespace {
 
-// A launch counts its blocks in 24 bits: one for every 128 rows of a key
-// head, and one for every sequence and key head.
+// A launch has fewer than 2^32 threads, 512 a block: one block for every 128
+// rows of a key head, and one for every sequence and key head.
 bool too_many_blocks(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_heads)
 {
-    return (n_tokens * (n_q_heads / n_k_heads) / 128 + n_seqs) * n_k_heads >= (1 << 24);
+    return (n_tokens * (n_q_heads / n_k_heads) / 128 + n_seqs) * n_k_heads >= (1 << 23);
 }
 
 }  // namespace

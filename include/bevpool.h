@@ -479,7 +479,7 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
  *       256-byte aligned, contents on entry ignored; calls that may overlap
  *       in time need one each.
  * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW (also n_tokens * n_q_heads / 128 +
- * n_seqs * n_k_heads from 2^24 on), WORKSPACE, HIP.
+ * n_seqs * n_k_heads from 2^23 on), WORKSPACE, HIP.
  */
 int bevpool_paged_attention(const void *q, int64_t q_stride, int32_t dtype, int64_t n_tokens,
                             int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,

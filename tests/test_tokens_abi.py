@@ -165,6 +165,15 @@ def test_workspace_sizes(lib):
         assert size(*bad) == 0, bad
 
 
+def test_attention_launch_fits(lib):
+    """Blocks of 512 threads, 2^32 threads a launch: up to 2^23 - 1 blocks."""
+    size = dws.bevpool_paged_attention_workspace_size
+    assert size(2, 2 ** 22 - 1, 2, 2, 16, 16, 1) > 0 and size(2, 2 ** 22, 2, 2, 16, 16, 1) == 0
+    assert attend_call(lib, seqs=2 ** 22, hq=2, hk=2) == OVERFLOW
+    assert size(2 ** 27, 1, 8, 1, 16, 16, 1) == 0            # 2^30 rows: 2^23 tiles
+    assert size(2 ** 27 - 256, 1, 8, 1, 16, 16, 1) > 0
+
+
 def test_binding_wants_gpu_tensors():
     q = torch.zeros(4, 2, 64)
     with pytest.raises(TypeError):

@@ -97,7 +97,9 @@ int check_rope(int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_h
     return BEVPOOL_OK;
 }
 
-bool good_scale(float s) { return s > 0.0f && std::isfinite(s); }
+// Of the scores: far enough from fp32's ends that the distance at which the
+// softmax's reference moves, 8 / scale, is finite.
+bool good_scale(float s) { return s >= 0x1p-96f && s <= 0x1p96f; }
 
 // far enough from fp32's ends that reciprocals and products stay normal
 bool good_cache_scale(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }

@@ -468,13 +468,15 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
  *
  * over the places j in [0, kv_lengths[s]) that are on a page and, with p the
  * place of token t, satisfy j <= p if causal and j > p - window if window > 0.
- * A token that sees no key gets 0.  Keys and values in hidden places have no
+ * A token that sees no key gets 0; a score of -infinity has weight 0, also
+ * where there are no others.  Keys and values in hidden places have no
  * influence, infinities and NaN among them.  Chunks, single tokens, or both
  * in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
  * statistics and sums are fp32; the weights enter the product with v rounded
  * to the token dtype (F16 for an FP8_E4M3 cache).
  *
- *   q, out: dtype F16 or BF16; scale positive and finite; window 0 = none.
+ *   q, out: dtype F16 or BF16; scale, and its product with k_scale, between
+ *       2^-96 and 2^96; window 0 = none.
  *   workspace: at least bevpool_paged_attention_workspace_size() bytes,
  *       256-byte aligned, contents on entry ignored; calls that may overlap
  *       in time need one each.

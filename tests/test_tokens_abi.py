@@ -135,6 +135,8 @@ def test_append_rejects(lib, kw, code):
     (dict(hq=0), INVALID), (dict(hq=9), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(cdt=E4M3, ks=2.0 ** 60, scale=2.0 ** 100), INVALID),
+    (dict(scale=1e-38), INVALID), (dict(scale=2.0 ** -97), INVALID), (dict(scale=2.0 ** 97), INVALID),
+    (dict(cdt=E4M3, ks=2.0 ** -60, scale=2.0 ** -40), INVALID),
     (dict(window=-1), INVALID), (dict(causal=2), INVALID), (dict(q=None), INVALID),
     (dict(out=None), INVALID), (dict(out=FAKE + 4), INVALID), (dict(os=1000), INVALID),
     (dict(ws=None), INVALID), (dict(ws=FAKE + 64), WORKSPACE), (dict(wsb=0), WORKSPACE)])

@@ -68,7 +68,8 @@ MAX_WINDOW = 2 ** 31 - 1             # past every place: as good as none
 class Rope:
     """Rotary positions of several axes: inv_freq [R/2] fp32 on the GPU, the
     number of pairs that turn with each axis (they add to R/2, a multiple of
-    8; none = no rotation), and which coordinates pair up."""
+    8; none = no rotation), and which coordinates pair up.  inv_freq's address
+    is taken here."""
     inv_freq: Optional[torch.Tensor]
     sections: Sequence[int] = ()
     layout: int = ROPE_HALVES
@@ -97,7 +98,8 @@ class Rope:
 class PagedCache:
     """Keys and values in pages: two contiguous tensors [n_pages, n_k_heads,
     page_size, head_dim] of float16, bfloat16 or e4m3 (float8_e4m3fn or its
-    uint8 codes, a stored value being code * scale)."""
+    uint8 codes, a stored value being code * scale).  Their addresses are taken
+    here: make another PagedCache after set_, resize_ or an assignment to .data."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: float = 1.0
@@ -124,7 +126,9 @@ class PagedCache:
 class PagedBatch:
     """The sequences of a batch, int32 on the GPU: q_offsets [n_seqs + 1] (new
     tokens of each), kv_lengths [n_seqs] (cached tokens of each, the new ones
-    among them) and block_table [n_seqs, max_pages] (their pages)."""
+    among them) and block_table [n_seqs, max_pages] (their pages).  Their values
+    may change between calls (a captured graph reads them anew), their
+    addresses are taken here."""
     q_offsets: torch.Tensor
     kv_lengths: torch.Tensor
     block_table: torch.Tensor

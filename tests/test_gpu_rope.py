@@ -187,6 +187,27 @@ def test_far_positions_keep_their_angle():
            np.concatenate([slack, slack], -1))
 
 
+@pytest.mark.parametrize("shape,dtype", [((20011, 3, 2, 128, (16, 24, 24), False), "bf16"),
+                                         ((50021, 2, 1, 48, (8, 8), True), "f32")])
+def test_backward_many_tokens(shape, dtype):
+    """More token groups than waves: each walks over several, and the weight
+    gradient is a sum over all of them."""
+    n, hq, hk, dim, sections, adjacent = shape
+    rng, rope, pos_t, pos, f, q, k, ws = _inputs(shape, dtype, True, 10)
+    dys = [values(rng, (n, h, dim), dtype) for h in (hq, hk)]
+    got = dws.bevpool_qk_norm_rope_backward(dys[0][0], dys[1][0], q[0], k[0], pos_t, rope,
+                                            ws[0][0], ws[1][0], EPS)
+    torch.cuda.synchronize()
+    for i, (dy, x, w) in enumerate(zip(dys, (q, k), ws)):
+        dx, dw = ref.norm_turn_backward(dy[1], x[1], w[1], EPS, pos, f, sections, adjacent)
+        bx, bw = _grad_bounds(dy[1], x[1], w[1], None, dx, dim, dtype, sum(sections), adjacent)
+        within(host(got[i]), dx, bx, "dx")
+        # the terms' own errors, and a sum of which a lane adds at most 2^7 terms in a
+        # row and the strips under 2^9 more: within 2^10 e of the sum of the sizes
+        bw = bw * (2.0 ** 10 + dim + 64) / (n * x[1].shape[1] + dim + 64)
+        within(host(got[2 + i]), dw, bw + U["f32"] * np.abs(dw), "dw")
+
+
 def test_in_place_and_given_outputs():
     shape = (50, 4, 2, 80, (8, 16, 16), False)
     _, rope, pos_t, pos, f, q, k, ws = _inputs(shape, "bf16", True, 6)

@@ -1175,17 +1175,19 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
     }
     // Many rows: the blocks run in rounds of `slots`.  In units' times of 128
     // rows, a block takes one or (256 rows, no waves that share keys) two for
-    // each unit, 6 or 8 to begin and end, and the join one.  Tiles of 128 rows
+    // each unit, 6 or 8 to begin and end, and the join one and more with its
+    // splits.  Tiles of 128 rows
     // against 256: 288 blocks of 2816 keys 90 us and 78, 1024 of up to 12288
     // 755 and 710, 228 of up to 6333 74 and 104 (the rule takes the better in
-    // each); 16 blocks of 8192 keys 131 us whole and 37 in 16 splits.
+    // each); 16 blocks of 8192 keys 131 us whole and 37 in 16 splits; one of
+    // 131072 keys (a token of 64 heads on one) 137 in 16 and 63 in up to 64.
     int64_t best = INT64_MAX;
     for (int tile_rows = 128; tile_rows <= (head_dim <= 128 ? 256 : 128); tile_rows *= 2) {
         const int64_t full = (rows + int64_t(n_seqs - 1) * (tile_rows / 2) + tile_rows - 1) / tile_rows *
                              n_k_heads;                    // about the tiles that have rows
-        for (int n = 1; n <= 16 && n <= units; ++n) {
+        for (int n = 1; n <= 64 && n <= units; ++n) {
             const int64_t block = (units + n - 1) / n * (tile_rows / 128) + 4 + tile_rows / 64;
-            const int64_t cost = (full * n + slots - 1) / slots * block + (n > 1);
+            const int64_t cost = (full * n + slots - 1) / slots * block + (n > 1 ? 1 + n / 16 : 0);
             if (cost >= best) continue;
             best = cost;
             s = {tile_rows, rows / tile_rows + n_seqs, n};

@@ -358,6 +358,17 @@ def test_attention_few_blocks_in_splits(dim, cache):
     _check_attention(b, q, 6, causal=False, window=2000)
 
 
+@pytest.mark.parametrize("new,ctx,hq,cache", [([1], [40000], 64, "bf16"), ([30], [20000], 6, "e4m3"),
+                                              ([1, 50], [17000, 10], 48, "bf16")])
+def test_attention_few_blocks_in_many_splits(new, ctx, hq, cache):
+    """One or two tiles of more than 32 rows over long contexts: more than 16
+    splits of each."""
+    rng = np.random.default_rng(38)
+    b = Batch(rng, new, ctx, 1, 64, 64, "bf16", cache)
+    q = values(rng, (b.n, hq, 64), "bf16", 1.5)
+    _check_attention(b, q, hq)
+
+
 @pytest.mark.parametrize("new,ctx", [([1], [200]), ([48], [152]), ([200], [100])])
 def test_attention_hidden_nan_codes(new, ctx):
     """The same of e4m3 caches, whose one value that is not finite is NaN."""

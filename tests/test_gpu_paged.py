@@ -412,6 +412,34 @@ def test_attention_graphs_that_share_a_workspace():
         assert torch.equal(eager, want[0])
 
 
+def test_attention_empty_and_wide_batches():
+    """No sequences, no tokens, a table of no pages, and one far wider than the
+    sequences need."""
+    rng = np.random.default_rng(39)
+    b = Batch(rng, [1, 40], [70, 30], 2, 64, 16, "bf16", "bf16")
+    q = values(rng, (b.n, 4, 64), "bf16")
+    none = torch.empty(0, dtype=torch.int32, device=dev())
+    zero = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = torch.full_like(q[0], 5.0)
+    empty = dws.PagedBatch(zero, none, none.view(0, 4))
+    assert (dws.bevpool_paged_attention(q[0], b.pool, empty, out=out) == 5).all()
+    got = dws.bevpool_paged_attention(q[0][:0], b.pool, b.batch)
+    assert got.shape == (0, 4, 64)
+    no_pages = dws.PagedBatch(b.batch.q_offsets, b.batch.kv_lengths, none.view(2, 0))
+    assert (dws.bevpool_paged_attention(q[0], b.pool, no_pages) == 0).all()
+    before = b.kt.clone()
+    kv = values(rng, (b.n, 2, 64), "bf16")[0]
+    dws.bevpool_kv_append(kv, kv, b.pool, no_pages, None, None)
+    dws.bevpool_kv_append(kv, kv, b.pool, empty, None, None)
+    dws.bevpool_kv_append(kv[:0], kv[:0], b.pool, b.batch, None, None)
+    assert torch.equal(_codes(b.kt).view(torch.int16), _codes(before).view(torch.int16))
+    wide = np.full((2, 20000), -1, np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    b.gpu()
+    _check_attention(b, q, 4)
+
+
 def test_attention_refusals():
     rng = np.random.default_rng(37)
     b = Batch(rng, [3, 40], [4, 9000], 2, 64, 16, "bf16", "bf16")

@@ -14,6 +14,12 @@
 // elements from 16j.  No coordinate moves between lanes; the mean square is
 // the only cross-lane sum.  A wave holds 64 / LPR tokens and walks over heads,
 // keeping its eight sines and cosines.
+//
+// Measured (a 2 GiB copy moves 4.96 TB/s): 16384 tokens of 16 + 4 heads of 128,
+// bf16: forward 41 us (4.1 TB/s), backward 53 us (4.7) and 4 for the last sum of
+// the weight gradient.  Append of 16384 tokens, 16 query heads, 8 key heads of
+// 128, bf16 to e4m3: 49 us (4.8 TB/s), of 64 single tokens 6 us: the chain
+// offsets, place, page, store.
 #include <hip/hip_runtime.h>
 
 #include "token_device.h"
@@ -335,12 +341,23 @@ __global__ __launch_bounds__(kBlock) void append(AppendParams a, int chunk)
     const int64_t t = there ? token : p.n_tokens - 1;
     const Slot s = slot_of(lane % LPR, p.head_dim, p.half, ADJ);
 
-    // the owner of each of the wave's tokens
+    // the owner of each of the wave's tokens: two searches where one a token
+    // took 16384 tokens of one sequence 48.7 us instead of 47.0, 64 of 64
+    // sequences 6.6 instead of 5.8
     const auto off = [&](int i) { return int64_t(clip(g.q_offsets[i], 0, p.n_tokens)); };
-    int seq = g.n_seqs;
-    for (int i = 0; i < kRows; ++i) {
-        const int found = count_upto(g.n_seqs, first + i, off);
-        if (lane / LPR == i) seq = found;
+    int seq = count_upto(g.n_seqs, first, off);
+    const int from = seq, more = count_upto(g.n_seqs, first + kRows - 1, off) - from;
+    if (more > 0 && more <= kLanes) {            // sequences that end among the wave's tokens
+        const int64_t ends = lane < more ? off(from + 1 + lane) : INT64_MAX;
+        for (int i = 1; i < kRows; ++i) {
+            const int found = from + __popcll(__ballot(ends <= first + i));
+            if (lane / LPR == i) seq = found;
+        }
+    } else if (more != 0) {                      // among them more empty ones than lanes
+        for (int i = 1; i < kRows; ++i) {
+            const int found = count_upto(g.n_seqs, first + i, off);
+            if (lane / LPR == i) seq = found;
+        }
     }
     bool owned = there && seq < g.n_seqs;
     const int q = owned ? seq : 0;

@@ -105,6 +105,24 @@ def test_append_drops_what_has_no_slot():
     within(host(got), want, turned_bound(q[1], 32, False, 64, "bf16", want))
 
 
+@pytest.mark.parametrize("dim", [16, 128])
+@pytest.mark.parametrize("empty", [3, 90])
+def test_append_many_empty_sequences(dim, empty):
+    """Sequences without new tokens between the tokens of one wave, fewer and
+    more than it has lanes."""
+    rng = np.random.default_rng(14)
+    new = [2] + [0] * empty + [5, 0, 0, 1, 60] + [0] * empty
+    b = Batch(rng, new, [3 * i % 40 for i in range(len(new))], 2, dim, 16, "bf16", "bf16", lead=3,
+              tail=2)
+    k, v = packed(rng, b.n, [2, 2], dim, "bf16")
+    before = b.kt.clone(), b.vt.clone()
+    got = dws.bevpool_kv_append(k[0], v[0], b.pool, b.batch, None, None)
+    torch.cuda.synchronize()
+    _check_append(b, got, before, k[1], v[1], k[1], 0, False)
+    q = values(rng, (b.n, 2, dim), "bf16")
+    _check_attention(b, q, 2, k=host(b.kt), v=host(b.vt))
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -64, 0.013, 2.0 ** 64])
 def test_append_e4m3_range(scale):
     """Values past 448 scales are cut, infinities too, NaN stays NaN."""

@@ -260,7 +260,9 @@ __global__ __launch_bounds__(kBlock) void norm_rope_bwd(RopeGradParams g, int ch
             rotate<ADJ>(ga, gb, cs, -sn, s.pair >= 0);
             if (weight) {
                 const float ms = row_sum<LPR>(dot8(xa, xa) + dot8(xb, xb)) * inv_dim;
-                const float r = 1.0f / sqrtf(ms + p.eps);
+                // lanes past the last token: their zeros over the root of eps = 0
+                // would put NaN into the weight's gradient
+                const float r = token < p.n_tokens ? 1.0f / sqrtf(ms + p.eps) : 0.0f;
                 xa *= r;
                 xb *= r;
                 da += ga * xa;

@@ -347,7 +347,7 @@ typedef enum bevpool_rope_layout {
  *   q, k: the input heads, dtype F32, F16 or BF16.  k may be NULL (n_k_heads
  *       then 0).  q_weight, k_weight [head_dim]: NULL = that one is not
  *       normed; weight_dtype is dtype or F32 (ignored when both are NULL).
- *   eps: at least 0 and finite.
+ *   eps: at least 0 and finite; with 0, a row of zeros is 0 / 0.
  *   positions [n_axes, n_tokens] int32, inv_freq [R/2] fp32; h_sections
  *       [n_axes] on the host, n_axes up to BEVPOOL_MAX_ROPE_AXES, 0 = no
  *       rotation (the three are then ignored).

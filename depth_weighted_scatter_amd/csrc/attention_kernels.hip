@@ -101,7 +101,8 @@ template <int DP> struct Tiles {
 // What a block works on.
 struct Plan {
     int seq, begin, q_len;     // sequence, its first token, its new tokens
-    int len;                   // its cached tokens
+    int len;                   // its cached tokens, at most the table's
+    int64_t place0;            // place of its first token, from lengths and offsets as they are
     int row0, rows;            // first row of the tile, rows in it
     int lo, hi;                // keys any of them sees: [lo, hi), lo a multiple of 64
     int per;                   // keys of one split
@@ -111,7 +112,7 @@ struct Plan {
 __device__ __forceinline__ void row_limits(const AttnParams &p, const Plan &w, int row, int group,
                                            int &lo, int &hi)
 {
-    const int64_t place = int64_t(w.len) - w.q_len + row / group;
+    const int64_t place = w.place0 + row / group;
     int64_t h = p.causal ? place + 1 : w.len, l = p.window > 0 ? place - p.window + 1 : 0;
     h = h < 0 ? 0 : (h > w.len ? w.len : h);
     l = l < 0 ? 0 : (l > w.len ? w.len : l);
@@ -145,6 +146,7 @@ __device__ __forceinline__ void plan_sequence(const AttnParams &p, Plan &w, int 
     w.begin = begin;
     w.q_len = end - begin;
     w.len = len < 0 ? 0 : (len < room ? len : int(room));
+    w.place0 = int64_t(len) - g.q_offsets[seq + 1] + begin;
 }
 
 // The sequence and first row of a tile, by the whole wave.  The tiles of

@@ -365,10 +365,10 @@ __global__ __launch_bounds__(kBlock) void append(AppendParams a, int chunk)
     const int q = owned ? seq : 0;
     const int begin = int(off(q)), end = int(off(q + 1));
     owned = owned && t >= begin && t < end;
-    // the token's slot
+    // the token's slot: its place follows from the length and the end of the
+    // sequence as they are, so one past the table is past it here
     const int64_t room = int64_t(g.max_pages) << g.page_shift;
-    const int64_t len = g.kv_lengths[q] < 0 ? 0 : (g.kv_lengths[q] < room ? g.kv_lengths[q] : room);
-    const int64_t place = len - (end - begin) + (t - begin);
+    const int64_t place = int64_t(g.kv_lengths[q]) - g.q_offsets[q + 1] + t;
     int page = -1;
     if (owned && place >= 0 && place < room)
         page = g.block_table[int64_t(q) * g.max_pages + (place >> g.page_shift)];

@@ -420,9 +420,10 @@ int bevpool_qk_norm_rope_backward(const void *dq_out, int64_t dq_out_stride, con
  *       pages that left the window, and mark them -1).
  * n_seqs is at most 2^24, max_pages * page_size at most 2^30; n_seqs *
  * max_pages and n_pages * page_size stay below 2^31 (else OVERFLOW).
- * Offsets are clipped to [0, n_tokens] and lengths to
- * [0, max_pages * page_size], so no value of these arrays makes a call read
- * or write outside its tensors.
+ * Places are taken from the arrays as they are, in 64 bits.  Places below 0
+ * or from max_pages * page_size on hold no key, and offsets beyond
+ * [0, n_tokens] name tokens that are not there: no value of these arrays makes
+ * a call read or write outside its tensors.
  */
 
 /*

@@ -52,13 +52,14 @@ def norm_turn_backward(dy, x, w, eps, positions, inv_freq, sections, adjacent):
 
 
 def places(offsets, lengths, max_pages, page, n_tokens):
-    """(sequence, place) of every token, (-1, 0) outside all of them."""
+    """(sequence, place) of every token, (-1, 0) outside all of them.  A place
+    may be negative or past the table; offsets may name tokens that are not
+    there."""
     seq, place = np.full(n_tokens, -1), np.zeros(n_tokens, np.int64)
     for s in range(len(lengths)):
         b, e = int(offsets[s]), int(offsets[s + 1])
-        kv = min(max(int(lengths[s]), 0), max_pages * page)
-        for t in range(b, e):
-            seq[t], place[t] = s, kv - (e - b) + t - b
+        for t in range(max(b, 0), min(e, n_tokens)):
+            seq[t], place[t] = s, int(lengths[s]) - (e - b) + t - b
     return seq, place
 
 
@@ -100,8 +101,8 @@ def attention(q, k_cache, v_cache, offsets, lengths, table, scale, causal, windo
         j, pages = j[there], pages[there]
         k = k_cache[pages, :, j % page].astype(np.float64)        # [keys, hk, dim]
         v = v_cache[pages, :, j % page].astype(np.float64)
-        for t in range(b, e):
-            p = kv - (e - b) + t - b
+        for t in range(max(b, 0), min(e, n)):
+            p = int(lengths[s]) - (e - b) + t - b
             see = np.ones(j.shape, bool)
             if causal:
                 see &= j <= p

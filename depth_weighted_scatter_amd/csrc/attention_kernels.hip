@@ -556,19 +556,34 @@ __device__ __forceinline__ float both_halves(float x)
                                          __builtin_bit_cast(float, uint32_t(r[1])));
 }
 
-// Takes the largest of a lane's scores into the running maximum.  The
+// Up to here a score times c is told from the reference times c in one
+// multiply-add: that product is rounded by at most 2^-13, which a weight shows
+// as 1 in 10^4, no more than the scores' own rounding.  Further out it would be
+// off by whole powers of two, and past 2^31 by all that fp32 holds.
+constexpr float kFar = 4096.0f;
+
+// Takes the largest of a lane's scores s into the running maximum.  The
 // reference moves only when a weight would pass 2^8: any reference within that
 // of the true maximum gives the same softmax, and most tiles then leave O as
-// it is, and ask no other lane.
+// it is, and ask no other lane.  With a reference past kFar in the wave, the
+// scores become differences to it here, in every tile (no score is below that
+// limit).
 template <int DP>
-__device__ __forceinline__ void move_top(Rows<DP> &r, float top, float c)
+__device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, float c)
 {
-    if (__any(top > r.limit)) {
+    if (__builtin_expect(__any(top > r.limit), 0)) {
         const float now = fmaxf(r.top, both_halves(top));
         const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
+        const float from = now == -INFINITY ? 0.0f : now;
         r.top = now;
-        r.base = now == -INFINITY ? 0.0f : now * c;
+        r.base = from * c;
         r.limit = now + 8.0f / c;
+        if (__builtin_expect(__any(fabsf(r.base) > kFar), 0)) {
+            r.base = 0.0f;
+            r.limit = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] -= from;
+        }
         r.sum *= keep;
 #pragma unroll
         for (int dt = 0; dt < Tiles<DP>::kDims; ++dt) {
@@ -707,7 +722,7 @@ __device__ __forceinline__ void store4(typename Elem<DT>::type *p, f32x4 v)
 }
 
 struct Parts {
-    float2 *stats;        // [splits][rows]: maximum * c, sum of weights
+    float2 *stats;        // [splits][rows]: maximum, sum of weights
     float *o;             // [splits][rows][head_dim]
     int64_t rows;         // n_tokens * n_q_heads
 };
@@ -834,13 +849,13 @@ struct RowWalk {
             }
             const bool hide_b = part_hidden(key0 + 32, there >> 2);
             const bool hide_a = part_hidden(key0 + kStride, next_there);
-            move_top<DP>(r, top, c);
+            move_top<DP>(r, a, top, c);
             scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, r.base, quarter(Const<0>{}));
             Ready<DP> ready = read_ahead<DP>(values);
             if (hide_b) hide(b, lo - key0 - 32, hi - key0 - 32, there >> 2);
             in_order();
             add_values<VT, DP, true>(r, x, values, ready, b, top, quarter(Const<1>{}));
-            move_top<DP>(r, top, c);
+            move_top<DP>(r, b, top, c);
             // in the last turn the next scores are of keys that nobody wants,
             // and so is their maximum
             scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, r.base, quarter(Const<2>{}));
@@ -907,7 +922,7 @@ struct KeyWalk {
             }
             const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
             if (!whole) hide(s, lo - key0, hi - key0, there);
-            move_top<DP>(r, largest(s), c);
+            move_top<DP>(r, s, largest(s), c);
             exponentials<VT>(s, x, r.sum, c, r.base, 0, 16);
             if constexpr (S::kDirect) {
                 if (more) wait_loads<S::kLoads>();
@@ -1070,7 +1085,7 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
         } else {
             const int64_t part = wave_rows[k0][col][1];
             *reinterpret_cast<f32x4 *>(parts.o + part * p.head_dim + d) = x;
-            if (d == 0) parts.stats[part] = make_float2(top * c, sum);
+            if (d == 0) parts.stats[part] = make_float2(top, sum);
         }
     }
 }
@@ -1082,14 +1097,14 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
 constexpr int kJoinBlock = 512;
 
 struct Sum {
-    float top, sum;      // maximum * c, sum of weights
+    float top, sum;      // maximum, sum of weights
     f32x4 o;
 };
 
-__device__ __forceinline__ float part_weight(float top, float all)
+__device__ __forceinline__ float part_weight(float top, float all, float c)
 {
     // scores that are all NaN leave no maximum, but a sum
-    return top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - all);
+    return top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((top - all) * c);
 }
 
 template <int DT>
@@ -1105,6 +1120,7 @@ __global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts pa
     plan_keys(p, w, group, tile_rows, max_splits);
     if (w.splits == 1) return;
 
+    const float c = p.scale * p.paged.k_scale * kLog2e;
     const int turn = int(gridDim.y), rows = (w.rows - int(blockIdx.y) + turn - 1) / turn;
     const int fours = p.head_dim / 4, n = rows * fours;
     int ways = 1;
@@ -1130,7 +1146,7 @@ __global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts pa
         for (int k = way; k < w.splits; k += ways) {
             const float2 st = stats[k * parts.rows];
             const f32x4 x = *reinterpret_cast<const f32x4 *>(o + k * parts.rows * p.head_dim);
-            const float f = st.y == 0.0f ? 0.0f : part_weight(st.x, a.top);   // 0: saw no key
+            const float f = st.y == 0.0f ? 0.0f : part_weight(st.x, a.top, c);   // 0: saw no key
             a.sum += st.y * f;
             a.o += x * f;
         }
@@ -1145,7 +1161,7 @@ __global__ __launch_bounds__(kJoinBlock) void attend_join(AttnParams p, Parts pa
     for (int k = 0; k < ways; ++k) a.top = fmaxf(a.top, shared[k * per_way + i].top);
     for (int k = 0; k < ways; ++k) {
         const Sum &b = shared[k * per_way + i];
-        const float f = b.sum == 0.0f ? 0.0f : part_weight(b.top, a.top);
+        const float f = b.sum == 0.0f ? 0.0f : part_weight(b.top, a.top, c);
         a.sum += b.sum * f;
         a.o += b.o * f;
     }

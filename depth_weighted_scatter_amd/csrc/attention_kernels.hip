@@ -49,6 +49,12 @@ typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 // exactly to either 16-bit type; fp16 rounds the weights 8 times finer.
 template <int DT, int CDT> struct Types { static constexpr int V = CDT == kE4M3 ? int(kF16) : DT; };
 
+// Weights, and so their sums, are 2^lift times what the reference makes them:
+// at most 2^15 (the reference may lie 2^8 low), inside fp16, which otherwise
+// would round those under 2^-25 to 0, however many there are; so it does those
+// under 2^-32.  The factor leaves with the division by the sum.
+template <int VT> constexpr float lift() { return VT == kF16 ? 7.0f : 0.0f; }
+
 template <int DT> struct Frag;
 template <> struct Frag<kF16> { using type = f16x8; };
 template <> struct Frag<kBF16> { using type = bf16x8; };
@@ -174,7 +180,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile
 // weights' sum.
 template <int DP> struct Rows {
     f32x16 o[Tiles<DP>::kDims];
-    float top, base, limit;     // reference; times c (0 without one); past this it moves
+    float top, base, limit;     // reference; times c less the lift; past this it moves
     float sum;
 
     __device__ Rows() : top(-INFINITY), base(0.0f), limit(-INFINITY), sum(0.0f)
@@ -568,7 +574,7 @@ constexpr float kFar = 4096.0f;
 // it is, and ask no other lane.  With a reference past kFar in the wave, the
 // scores become differences to it here, in every tile (no score is below that
 // limit).
-template <int DP>
+template <int VT, int DP>
 __device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, float c)
 {
     if (__builtin_expect(__any(top > r.limit), 0)) {
@@ -576,10 +582,10 @@ __device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, floa
         const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
         const float from = now == -INFINITY ? 0.0f : now;
         r.top = now;
-        r.base = from * c;
+        r.base = fmaf(from, c, -lift<VT>());
         r.limit = now + 8.0f / c;
         if (__builtin_expect(__any(fabsf(r.base) > kFar), 0)) {
-            r.base = 0.0f;
+            r.base = -lift<VT>();
             r.limit = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] -= from;
@@ -849,13 +855,13 @@ struct RowWalk {
             }
             const bool hide_b = part_hidden(key0 + 32, there >> 2);
             const bool hide_a = part_hidden(key0 + kStride, next_there);
-            move_top<DP>(r, a, top, c);
+            move_top<VT, DP>(r, a, top, c);
             scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, r.base, quarter(Const<0>{}));
             Ready<DP> ready = read_ahead<DP>(values);
             if (hide_b) hide(b, lo - key0 - 32, hi - key0 - 32, there >> 2);
             in_order();
             add_values<VT, DP, true>(r, x, values, ready, b, top, quarter(Const<1>{}));
-            move_top<DP>(r, b, top, c);
+            move_top<VT, DP>(r, b, top, c);
             // in the last turn the next scores are of keys that nobody wants,
             // and so is their maximum
             scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, r.base, quarter(Const<2>{}));
@@ -922,7 +928,7 @@ struct KeyWalk {
             }
             const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
             if (!whole) hide(s, lo - key0, hi - key0, there);
-            move_top<DP>(r, s, largest(s), c);
+            move_top<VT, DP>(r, s, largest(s), c);
             exponentials<VT>(s, x, r.sum, c, r.base, 0, 16);
             if constexpr (S::kDirect) {
                 if (more) wait_loads<S::kLoads>();

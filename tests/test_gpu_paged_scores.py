@@ -1,5 +1,5 @@
 """Attention where the size of the scores decides: very large ones, whose
-softmax is one key."""
+softmax is one key, and many small weights beside a large one."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +70,33 @@ def test_attention_of_one_key(case, dim, dtype, cache):
         assert (off <= want.abs().double() * (torch.finfo(DT[dtype]).eps / 2 + 2.0 ** -22)).all()
     else:
         assert torch.equal(got.cpu(), want.to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dim,cache", [(64, "f16"), (128, "e4m3")])
+@pytest.mark.parametrize("n,hq,hk", [(8192, 8, 8), (2, 16, 8)])
+def test_attention_many_small_weights(n, hq, hk, dim, cache):
+    """One key of weight 1 and value 0, and 2^16 of weight 2^-27 and value 1,
+    which fp16 alone would round to 0.  Weights reach the product with v as
+    fp16 numbers 2^7 times as large, so one under 2^-21 is off by up to 2^-32
+    and the sum by 2^16 * 2^-32; the rest are a few roundings of it."""
+    keys, page = 65536, 64
+    rng = np.random.default_rng(72)
+    k_scale, v_scale = (0.5, 0.25) if cache == "e4m3" else (1.0, 1.0)
+    kt = torch.zeros((keys // page, hk, page, dim), device=dev())
+    vt = torch.full_like(kt, 1.0 / v_scale)
+    kt[0, :, 0, 0] = 16.0 / k_scale
+    vt[0, :, 0] = 0.0
+    pool = dws.PagedCache(kt.to(DT[cache]), vt.to(DT[cache]), k_scale, v_scale)
+    del kt, vt
+    batch = dws.PagedBatch(torch.tensor([0, n], dtype=torch.int32, device=dev()),
+                           torch.tensor([keys], dtype=torch.int32, device=dev()),
+                           torch.arange(keys // page, dtype=torch.int32, device=dev())[None])
+    q = torch.zeros((n, hq, dim), dtype=torch.float16, device=dev())
+    q[..., 0] = 1.0
+    got = dws.bevpool_paged_attention(q, pool, batch, 27 * np.log(2.0) / 16, causal=False)
+    tail = (keys - 1) * 2.0 ** -27
+    want = tail / (1 + tail)
+    # the scale is an fp32 number and so is its product with log2 e: 27 of them are within 2^-18
+    slack = keys * 2.0 ** -32 + want * (2.0 ** -11 + 2.0 ** -18 + 2.0 ** -16)
+    off = (got.double() - want).abs().max().item()
+    assert off <= slack, (off, slack, want)

@@ -454,7 +454,7 @@ struct Stage {
     // Of the pieces this wave has read, before the others see them: values of
     // places that no row sees become zeros (the tail of a
     // page may hold anything, and 0 * NaN is not 0); so do infinities and NaN
-    // that some rows see and others do not, which set bad.
+    // that some rows see and others do not, whose first and last key bad gets.
     __device__ __forceinline__ void clean_values(char *lds, int tile, uint32_t there, int *bad) const
     {
         const int key0 = first + tile * stride;
@@ -464,7 +464,8 @@ struct Stage {
                 *x = 0;
             } else if (non_finite<VT>(*x)) {
                 *x = finite_only<VT>(*x);
-                *bad = 1;
+                atomicMin(&bad[0], key0 + key);
+                atomicMax(&bad[1], key0 + key);
             }
         });
     }
@@ -695,7 +696,9 @@ __device__ __forceinline__ void add_values(Rows<DP> &r, const u32x4 (&w)[2], con
 
 // The infinities and NaN of four dims among the values that a row sees, added
 // up (0 if there are none): any weight times one of them is it.  Keys in
-// [lo, hi) that are on a page.
+// [lo, hi) that are on a page: those between the first and the last such value
+// that was taken out (over all keys of a block, one infinity in the last place
+// made 4096 tokens over 12288 keys take 62 ms instead of 0.7).
 template <int CDT>
 __device__ f32x4 non_finite_sum(const AttnParams &p, const int32_t *table, int kv_head, int d,
                                 int lo, int hi)
@@ -952,7 +955,7 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
     using L = Tiles<DP>;
     constexpr int kWaves = L::kWaves;
     __shared__ __attribute__((aligned(16))) char lds[L::kLds];
-    __shared__ int bad;          // a hidden place may hold a value that is not finite
+    __shared__ int bad[2];       // keys between which values that are not finite were taken out
     __shared__ float wave_stats[kWaves][32][2];
     __shared__ int64_t wave_rows[kWaves][32][2];
 
@@ -992,7 +995,7 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
         wave_rows[wave][col][1] = split * parts.rows + int64_t(token) * p.n_q_heads + head;
     }
     const float c = p.scale * g.k_scale * kLog2e;
-    if (threadIdx.x == 0) bad = 0;
+    if (threadIdx.x < 2) bad[threadIdx.x] = threadIdx.x == 0 ? INT32_MAX : -1;
     __syncthreads();
 
     u32x4 q[L::kSteps];
@@ -1016,15 +1019,15 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
     if (ways == 1) {
         RowWalk<DT, CDT, DP, EXACT, 1> walk(p, w, kv_head, wave, from, to, lds);
         read_queries();
-        walk.run(group, lo, hi, c, q, &bad, r);
+        walk.run(group, lo, hi, c, q, bad, r);
     } else if (ways == 2) {
         RowWalk<DT, CDT, DP, EXACT, kWaves == 8 ? 2 : 1> walk(p, w, kv_head, wave, from, to, lds);
         read_queries();
-        walk.run(group, lo, hi, c, q, &bad, r);
+        walk.run(group, lo, hi, c, q, bad, r);
     } else {
         KeyWalk<DT, CDT, DP, EXACT> walk(p, w, kv_head, wave, from, to, lds);
         read_queries();
-        walk.run(lo, hi, c, q, &bad, r);
+        walk.run(lo, hi, c, q, bad, r);
     }
     r.sum += __shfl_xor(r.sum, 32);
 
@@ -1061,7 +1064,7 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
     // four dims a lane, a row to 32 or 64 lanes
     constexpr int kRowLanes = DP <= 128 ? 32 : 64, kRowsAtOnce = kWaves * kLanes / kRowLanes;
     const int d = int(threadIdx.x) % kRowLanes * 4;
-    const bool look = bad != 0;
+    const int bad_lo = bad[0], bad_hi = bad[1] + 1;
     for (int n = int(threadIdx.x) / kRowLanes; n < w.rows; n += kRowsAtOnce) {
         if (d >= p.head_dim) continue;
         const int k0 = n / 32, col = n % 32;
@@ -1079,11 +1082,11 @@ __global__ __launch_bounds__(Tiles<DP>::kWaves *kLanes, DP > 128 ? 1 : 2) void a
                 if (part != 0.0f) sum += part * weight(wave_stats[k][col][0], top);
             }
         }
-        if (look) {
+        if (bad_lo < bad_hi) {
             int lo, hi;
             row_limits(p, w, w.row0 + n, group, lo, hi);
             x += non_finite_sum<CDT>(p, g.block_table + int64_t(w.seq) * g.max_pages, kv_head, d,
-                                     max(lo, from), min(hi, to));
+                                     max(lo, bad_lo), min(hi, bad_hi));
         }
         if (w.splits == 1) {
             x *= sum == 0.0f ? 0.0f : g.v_scale / sum;

@@ -316,8 +316,8 @@ int bevpool_forward_baseline(int32_t order, const void *depth, int32_t depth_dty
  *     elements, a multiple of 16 bytes, at least heads * head_dim), so
  *     queries, keys and values may be slices of one packed projection.
  *     Tensors are 16-byte aligned.
- *   - Arithmetic is fp32 (angles: fp64); every result is rounded once, to
- *     nearest-even, to its output type.
+ *   - Arithmetic is fp32 (angles: fp64) except where a call says otherwise;
+ *     every result is rounded once, to nearest-even, to its output type.
  *   - A call with zero tokens does nothing and returns BEVPOOL_OK (the
  *     backward still writes zero weight gradients).
  *   - Asynchronous on `stream`, no allocation, capturable in a HIP graph.
@@ -471,10 +471,14 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
  * place of token t, satisfy j <= p if causal and j > p - window if window > 0.
  * A token that sees no key gets 0; a score of -infinity has weight 0, also
  * where there are no others.  Keys and values in hidden places have no
- * influence, infinities and NaN among them.  Chunks, single tokens, or both
- * in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
+ * influence, infinities and NaN among them.  A coordinate of an output is
+ * finite exactly if that coordinate of every value the token sees is, whatever
+ * their weights; whether it is infinite or NaN otherwise is not specified (a
+ * weight that rounds to 0 may make NaN of an infinity).  Chunks, single tokens,
+ * or both in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
  * statistics and sums are fp32; the weights enter the product with v rounded
- * to the token dtype (F16 for an FP8_E4M3 cache).
+ * to BF16 for a BF16 cache and to F16 for the others, the sum they are divided
+ * by takes them unrounded (F16 weights below 2^-32 of the largest count as 0).
  *
  *   q, out: dtype F16 or BF16; scale, and its product with k_scale, between
  *       2^-96 and 2^96; window 0 = none.

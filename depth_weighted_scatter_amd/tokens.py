@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
+import inspect
 from typing import Optional, Sequence
 
 import torch
@@ -267,22 +268,31 @@ def _on_device(call):
     """Runs call with its first tensor's device current and, where stream is
     given, with that stream current; the arguments are then marked as used on
     it, so none is recycled while the work is pending."""
+    signature = inspect.signature(call)
+    name = next(iter(signature.parameters))
+
     @functools.wraps(call)
-    def run(first, *args, stream=None, **kw):
+    def run(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise TypeError("the first argument must be a GPU tensor")
+            if not args and name not in kw:
+                return call(*args, **kw)         # its own error: the argument is missing
+            raise TypeError(f"{name} must be a GPU tensor")
         if stream is None:
             if first.get_device() == _current_device():
-                return call(first, *args, **kw)
+                return call(*args, **kw)
             with torch.cuda.device(first.device):
-                return call(first, *args, **kw)
+                return call(*args, **kw)
         if stream.device != first.device:
             raise ValueError("stream and tensors are on different devices")
         with torch.cuda.stream(stream):
-            got = call(first, *args, **kw)
-        for t in _tensors((first, *args, *kw.values())):
+            got = call(*args, **kw)
+        for t in _tensors((*args, *kw.values())):
             t.record_stream(stream)
         return got
+    run.__signature__ = signature.replace(parameters=[
+        *signature.parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return run
 
 

@@ -296,12 +296,71 @@ def _on_device(call):
     return run
 
 
+def _wants_gradient(*tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return True
+    return False
+
+
+def _no_gradient(call, why, *tensors):
+    # A call without a gradient must not cut a graph in silence.
+    if _wants_gradient(*tensors):
+        raise RuntimeError(f"{call}: {why}; call it under torch.no_grad() or detach its arguments")
+
+
 def _raw_stream(t):
     # the handle of the current stream of t's device, without a Stream object
     return _current_stream(t.get_device())
 
 
 # ---- calls ----------------------------------------------------------------------------------
+def _gradient_rows(t):
+    # A gradient as autograd may hand it on (expanded, transposed, part of a
+    # tensor), in rows that the call takes.
+    n, heads, dim = t.shape
+    st, sh, sd = t.stride()
+    if (sd == 1 and (sh == dim or heads == 1) and t.data_ptr() % 16 == 0 and
+            (n <= 1 or (st >= heads * dim and st * t.element_size() % 16 == 0))):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, rope, eps):
+        turns = rope is not None and rope.sections
+        # the inputs are read again where there is a weight only
+        ctx.save_for_backward(q if q_weight is not None else None,
+                              k if k_weight is not None else None, q_weight, k_weight,
+                              positions if turns else None, rope.inv_freq if turns else None)
+        ctx.rope, ctx.eps, ctx.has_k = rope, eps, k is not None
+        ctx.like = q.shape, q.dtype, q.device
+        ctx.set_materialize_grads(False)
+        return _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions, _ = ctx.saved_tensors
+        need_q, need_k, need_qw, need_kw = ctx.needs_input_grad[:4]
+        if dq_out is None and dk_out is None:
+            return (None,) * 7
+        if dq_out is None:
+            shape, dtype, device = ctx.like
+            dq_out = torch.zeros(shape, dtype=dtype, device=device)
+        if dk_out is None or not (need_k or need_kw):
+            dk_out = k = k_weight = None
+        else:
+            dk_out = _gradient_rows(dk_out)
+        dq, dk, dqw, dkw = bevpool_qk_norm_rope_backward(
+            _gradient_rows(dq_out), dk_out, q, k, positions, ctx.rope, q_weight, k_weight, ctx.eps)
+        return (dq if need_q else None, dk if need_k else None,
+                dqw.to(q_weight.dtype) if need_qw else None,
+                dkw.to(k_weight.dtype) if need_kw and dkw is not None else None, None, None, None)
+
+
 @_on_device
 def bevpool_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
                          positions: Optional[torch.Tensor], rope: Optional[Rope],
@@ -313,7 +372,26 @@ def bevpool_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     (q_out, k_out).  q, k: [n_tokens, heads, head_dim] float32, float16 or
     bfloat16, heads contiguous, any token stride (slices of a packed
     projection); k may be None.  positions: int32 [axes, n_tokens].  An
-    output may be its input.  Keyword stream: where to run."""
+    output may be its input.  Keyword stream: where to run.
+
+    Differentiable in q, k and the weights (bevpool_qk_norm_rope_backward, the
+    weights' gradients rounded once to their type); there is no second
+    derivative.  Where a gradient is wanted the outputs are new tensors, and
+    the call is not captured in a graph: capture it under torch.no_grad() and
+    bevpool_qk_norm_rope_backward after it."""
+    if _wants_gradient(q, k, q_weight, k_weight, q_out, k_out):
+        if q_out is not None or k_out is not None:
+            raise RuntimeError("bevpool_qk_norm_rope: q_out and k_out are not differentiable; leave "
+                               "them out or call it under torch.no_grad()")
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("bevpool_qk_norm_rope: its graph of gradients is not captured; call "
+                               "it under torch.no_grad(), then bevpool_qk_norm_rope_backward")
+        return _QkNormRope.apply(q, k, q_weight, None if k is None else k_weight, positions, rope,
+                                 eps)
+    return _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out)
+
+
+def _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out):
     lib = _lib()
     sq = _token_rows("q", q)
     n, hq, dim = q.shape
@@ -358,7 +436,10 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
     and None without a weight.  q and k are needed with their weight only; dq
     may be dq_out, dk may be dk_out.  workspace: uint8, at least
     bevpool_qk_norm_rope_backward_workspace_size bytes; made here when None.
-    Keyword stream: where to run."""
+    Keyword stream: where to run.  The gradients carry no graph; one that is
+    asked for (dq_out or dk_out with requires_grad) is refused."""
+    _no_gradient("bevpool_qk_norm_rope_backward", "there is no second derivative", dq_out, dk_out,
+                 dq, dk)
     lib = _lib()
     _token_rows("dq_out", dq_out)
     n, hq, dim = dq_out.shape
@@ -409,7 +490,10 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
     into the cache's pages; normes and rotates the queries q, if given, in the
     same launch and returns them.  k, v, q: [n_tokens, heads, head_dim] float16
     or bfloat16.  Rows of q_out outside every sequence are left as they were.
-    Keyword stream: where to run."""
+    Keyword stream: where to run.  It has no gradient: arguments with
+    requires_grad are refused where gradients are on."""
+    _no_gradient("bevpool_kv_append", "it has no gradient", k, v, q, q_weight, k_weight, q_out,
+                 cache.k, cache.v)
     lib = _lib()
     sk = _token_rows("k", k)
     sv = _token_rows("v", v, k)
@@ -456,7 +540,9 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
     out outside every sequence are left as they were.  workspace: uint8, at
     least bevpool_paged_attention_workspace_size bytes; made here when None;
     calls that may overlap in time need one each.  Keyword stream: where to
-    run."""
+    run.  It has no gradient: arguments with requires_grad are refused where
+    gradients are on."""
+    _no_gradient("bevpool_paged_attention", "it has no gradient", q, out, cache.k, cache.v)
     lib = _lib()
     sq = _token_rows("q", q)
     n, hq, dim = q.shape

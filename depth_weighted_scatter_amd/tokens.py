@@ -310,6 +310,14 @@ def _no_gradient(call, why, *tensors):
         raise RuntimeError(f"{call}: {why}; call it under torch.no_grad() or detach its arguments")
 
 
+def _written(*tensors):
+    # Tells autograd that the caller's tensors were written in place (None: a
+    # new one was made), so that it notices where it had kept one.
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _raw_stream(t):
     # the handle of the current stream of t's device, without a Stream object
     return _current_stream(t.get_device())
@@ -393,6 +401,7 @@ def bevpool_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
 
 def _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out):
     lib = _lib()
+    given = q_out, k_out
     sq = _token_rows("q", q)
     n, hq, dim = q.shape
     if q.dtype not in _TOKEN_DTYPE:
@@ -413,6 +422,7 @@ def _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out):
         _raw_stream(q))
     if rc != OK:
         raise BevPoolError("bevpool_qk_norm_rope", rc)
+    _written(*given)
     return q_out, k_out
 
 
@@ -441,6 +451,7 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
     _no_gradient("bevpool_qk_norm_rope_backward", "there is no second derivative", dq_out, dk_out,
                  dq, dk)
     lib = _lib()
+    given = dq, dk
     _token_rows("dq_out", dq_out)
     n, hq, dim = dq_out.shape
     if dq_out.dtype not in _TOKEN_DTYPE:
@@ -477,6 +488,7 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
         None if dkw is None else dkw.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dq_out))
     if rc != OK:
         raise BevPoolError("bevpool_qk_norm_rope_backward", rc)
+    _written(*given)
     return dq, dk, dqw, dkw
 
 
@@ -495,6 +507,7 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
     _no_gradient("bevpool_kv_append", "it has no gradient", k, v, q, q_weight, k_weight, q_out,
                  cache.k, cache.v)
     lib = _lib()
+    given = q_out
     sk = _token_rows("k", k)
     sv = _token_rows("v", v, k)
     n, hk, dim = k.shape
@@ -519,6 +532,7 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
         *_paged_args(k, cache, batch), _raw_stream(k))
     if rc != OK:
         raise BevPoolError("bevpool_kv_append", rc)
+    _written(given, cache.k, cache.v)
     return q_out
 
 
@@ -548,7 +562,7 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
     n, hq, dim = q.shape
     if q.dtype not in _TOKEN_DTYPE:
         raise TypeError(f"q must be float16 or bfloat16, got {q.dtype}")
-    paged = _paged_args(q, cache, batch)
+    paged, given = _paged_args(q, cache, batch), out
     hk, page = cache._shape[1], cache._shape[2]
     out, so = _output("out", out, q)
     ws = _workspace(lib.bevpool_paged_attention_workspace_size(
@@ -560,4 +574,5 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
         min(max(int(window), -1), MAX_WINDOW), out.data_ptr(), so, ws.data_ptr(), ws.numel(), _raw_stream(q))
     if rc != OK:
         raise BevPoolError("bevpool_paged_attention", rc)
+    _written(given)
     return out

@@ -35,9 +35,10 @@ int check_sizes(int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t 
     if (n_tokens < 0 || n_q_heads < 0 || n_k_heads < 0 || head_dim <= 0)
         return BEVPOOL_ERR_INVALID_ARG;
     if (head_dim % 16 != 0 || head_dim > kMaxHeadDim) return BEVPOOL_ERR_UNSUPPORTED;
-    // the second bound keeps a launch's threads (at most n_tokens * head_dim / 8)
-    // within the 32 bits of a grid
-    if (n_tokens > kInt32Limit || n_tokens * (int64_t(n_q_heads) + 2 * int64_t(n_k_heads)) > kInt32Limit ||
+    // heads are bounded first, so that no product wraps; the last bound keeps a
+    // launch's threads (at most n_tokens * head_dim / 8) within the 32 bits of a grid
+    const int64_t heads = int64_t(n_q_heads) + 2 * int64_t(n_k_heads);
+    if (n_tokens > kInt32Limit || heads > kInt32Limit || n_tokens * heads > kInt32Limit ||
         n_tokens * head_dim > (int64_t(1) << 34))
         return BEVPOOL_ERR_OVERFLOW;
     return BEVPOOL_OK;
@@ -47,9 +48,9 @@ int check_sizes(int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads, int32_t 
 // stride that covers its heads and keeps rows 16-byte aligned.
 int check_rows(const void *x, int64_t stride, int32_t heads, int32_t head_dim, int bytes)
 {
-    if (!x || !aligned(x, 16) || stride < int64_t(heads) * head_dim || (stride * bytes) % 16 != 0)
-        return BEVPOOL_ERR_INVALID_ARG;
-    return stride > (int64_t(1) << 31) ? BEVPOOL_ERR_OVERFLOW : BEVPOOL_OK;
+    if (!x || !aligned(x, 16) || stride < int64_t(heads) * head_dim) return BEVPOOL_ERR_INVALID_ARG;
+    if (stride > (int64_t(1) << 31)) return BEVPOOL_ERR_OVERFLOW;
+    return (stride * bytes) % 16 != 0 ? BEVPOOL_ERR_INVALID_ARG : BEVPOOL_OK;
 }
 
 // Norm and rotation arguments; fills the fields of p that do not name token

@@ -354,8 +354,8 @@ typedef enum bevpool_rope_layout {
  *   q_out, k_out: dtype; each may be its input (same pointer and stride),
  *       otherwise they do not overlap any input.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, weight_dtype, head_dim, R),
- * OVERFLOW (n_tokens * (n_q_heads + 2 n_k_heads) beyond 2^31 - 1, n_tokens *
- * head_dim beyond 2^34, a stride beyond 2^31), HIP.
+ * OVERFLOW (n_q_heads + 2 n_k_heads, or n_tokens times it, beyond 2^31 - 1,
+ * n_tokens * head_dim beyond 2^34, a stride beyond 2^31), HIP.
  */
 int bevpool_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                          int32_t dtype, int64_t n_tokens, int32_t n_q_heads, int32_t n_k_heads,

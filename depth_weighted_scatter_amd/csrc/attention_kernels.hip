@@ -180,7 +180,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, Plan &w, int tile
 // weights' sum.
 template <int DP> struct Rows {
     f32x16 o[Tiles<DP>::kDims];
-    float top, base, limit;     // reference; times c less the lift; past this it moves
+    float top, base, limit;     // reference; what exponents are told from; past this it moves
     float sum;
 
     __device__ Rows() : top(-INFINITY), base(0.0f), limit(-INFINITY), sum(0.0f)
@@ -563,19 +563,24 @@ __device__ __forceinline__ float both_halves(float x)
                                          __builtin_bit_cast(float, uint32_t(r[1])));
 }
 
-// Up to here a score times c is told from the reference times c in one
-// multiply-add: that product is rounded by at most 2^-13, which a weight shows
-// as 1 in 10^4, no more than the scores' own rounding.  Further out it would be
-// off by whole powers of two, and past 2^31 by all that fp32 holds.
+// The exponent of a weight is (score - reference) c + lift.  Near zero (ONE) it
+// takes one multiply-add, score * c less the reference times c: that product is
+// rounded, up to kFar by at most 2^-13, which a weight shows as 1 in 10^4, no
+// more than the scores' own rounding.  Further out it would be off by whole
+// powers of two, and past 2^31 by all that fp32 holds: there the scores become
+// differences to the reference first.  Where instructions are not what bounds a
+// walk, or a second path costs it registers, every weight takes the difference
+// (64 single tokens of up to 8192 keys 249 us with ONE, 244 without; 2 x 1024
+// tokens over 4096 keys, 16 heads of 256 on 4, bf16 297 and 240, e4m3 371 and
+// 379).
 constexpr float kFar = 4096.0f;
 
 // Takes the largest of a lane's scores s into the running maximum.  The
 // reference moves only when a weight would pass 2^8: any reference within that
 // of the true maximum gives the same softmax, and most tiles then leave O as
-// it is, and ask no other lane.  With a reference past kFar in the wave, the
-// scores become differences to it here, in every tile (no score is below that
-// limit).
-template <int VT, int DP>
+// it is, and ask no other lane.  With ONE and a reference past kFar in the
+// wave, no score is below the limit and every tile comes here.
+template <int VT, int DP, bool ONE>
 __device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, float c)
 {
     if (__builtin_expect(__any(top > r.limit), 0)) {
@@ -583,13 +588,15 @@ __device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, floa
         const float keep = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((r.top - now) * c);
         const float from = now == -INFINITY ? 0.0f : now;
         r.top = now;
-        r.base = fmaf(from, c, -lift<VT>());
+        r.base = ONE ? fmaf(from, c, -lift<VT>()) : from;
         r.limit = now + 8.0f / c;
-        if (__builtin_expect(__any(fabsf(r.base) > kFar), 0)) {
-            r.base = -lift<VT>();
-            r.limit = -INFINITY;
+        if constexpr (ONE) {
+            if (__builtin_expect(__any(fabsf(r.base) > kFar), 0)) {
+                r.base = -lift<VT>();
+                r.limit = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] -= from;
+                for (int i = 0; i < 16; ++i) s[i] -= from;
+            }
         }
         r.sum *= keep;
 #pragma unroll
@@ -602,14 +609,14 @@ __device__ __forceinline__ void move_top(Rows<DP> &r, f32x16 &s, float top, floa
 
 // Scores [from, to) of 32 keys to weights, added to sum; pairs are rounded to
 // VT once both are there.
-template <int VT>
+template <int VT, bool ONE>
 __device__ __forceinline__ void exponentials(f32x16 &s, u32x4 (&w)[2], float &sum, float c, float base,
                                              int from, int to)
 {
     typedef typename Elem<VT>::type V2 __attribute__((ext_vector_type(2)));
 #pragma unroll
     for (int n = from; n < to; ++n) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(s[n], c, -base));
+        const float x = __builtin_amdgcn_exp2f(ONE ? fmaf(s[n], c, -base) : fmaf(s[n] - base, c, lift<VT>()));
         s[n] = x;
         sum += x;
         if (n % 2) {
@@ -632,7 +639,7 @@ struct NoLoads {
 // 32 keys before (BESIDE): a wave issues one and goes on, and 16 scores take
 // about as long as the head's instructions do; loads(n, kN) issues what is to be
 // issued beside the n-th of kN.
-template <int DT, int VT, int DP, bool BESIDE, typename Loads>
+template <int DT, int VT, int DP, bool BESIDE, bool ONE, typename Loads>
 __device__ __forceinline__ void scores(f32x16 &out, const u32x4 (&q)[Tiles<DP>::kSteps],
                                        const char *keys, f32x16 &s, u32x4 (&w)[2], float &sum, float c,
                                        float base, Loads loads)
@@ -648,7 +655,7 @@ __device__ __forceinline__ void scores(f32x16 &out, const u32x4 (&q)[Tiles<DP>::
     for (int n = 0; n < kN; ++n) {
         o = mfma<DT>(a[n % kAhead], q[n], o);
         if (n + kAhead < kN) a[n % kAhead] = read(n + kAhead);
-        if constexpr (BESIDE) exponentials<VT>(s, w, sum, c, base, n * 16 / kN, (n + 1) * 16 / kN);
+        if constexpr (BESIDE) exponentials<VT, ONE>(s, w, sum, c, base, n * 16 / kN, (n + 1) * 16 / kN);
         loads(n, kN);
         in_order();
     }
@@ -751,6 +758,7 @@ struct RowWalk {
     using L = Tiles<DP>;
     static constexpr int VT = Types<DT, CDT>::V, kWaves = L::kWaves / WAYS;
     static constexpr int kHalf = 32 * L::kRow, kTile = 2 * kHalf, kStride = 64 * WAYS;
+    static constexpr bool kOne = DP <= 128 || CDT == kE4M3;          // of move_top
     using Keys = Stage<DT, CDT, DP, EXACT, kWaves, true>;
     using Vals = Stage<DT, CDT, DP, EXACT, kWaves, false>;
 
@@ -844,7 +852,7 @@ struct RowWalk {
 
         begin(-1, lds, lds);                  // brings the first 32 keys
         all_loads();
-        scores<DT, VT, DP, false>(a, q, lds + kHalf, b, x, none, c, 0.0f, NoLoads{});
+        scores<DT, VT, DP, false, kOne>(a, q, lds + kHalf, b, x, none, c, 0.0f, NoLoads{});
         hide(a, lo - first, hi - first, next_there);
         top = largest(a);
         for (int t = 0; t < n_turns; ++t) {
@@ -858,16 +866,16 @@ struct RowWalk {
             }
             const bool hide_b = part_hidden(key0 + 32, there >> 2);
             const bool hide_a = part_hidden(key0 + kStride, next_there);
-            move_top<VT, DP>(r, a, top, c);
-            scores<DT, VT, DP, true>(b, q, keys, a, x, r.sum, c, r.base, quarter(Const<0>{}));
+            move_top<VT, DP, kOne>(r, a, top, c);
+            scores<DT, VT, DP, true, kOne>(b, q, keys, a, x, r.sum, c, r.base, quarter(Const<0>{}));
             Ready<DP> ready = read_ahead<DP>(values);
             if (hide_b) hide(b, lo - key0 - 32, hi - key0 - 32, there >> 2);
             in_order();
             add_values<VT, DP, true>(r, x, values, ready, b, top, quarter(Const<1>{}));
-            move_top<VT, DP>(r, b, top, c);
+            move_top<VT, DP, kOne>(r, b, top, c);
             // in the last turn the next scores are of keys that nobody wants,
             // and so is their maximum
-            scores<DT, VT, DP, true>(a, q, keys + kHalf, b, x, r.sum, c, r.base, quarter(Const<2>{}));
+            scores<DT, VT, DP, true, kOne>(a, q, keys + kHalf, b, x, r.sum, c, r.base, quarter(Const<2>{}));
             ready = read_ahead<DP>(values + kHalf);
             if (hide_a) hide(a, lo - key0 - kStride, hi - key0 - kStride, next_there);
             in_order();
@@ -922,7 +930,7 @@ struct KeyWalk {
                 st.template store<false>(keys);
                 st.template store<true>(values);
             }
-            scores<DT, VT, DP, false>(s, q, keys, s, x, r.sum, c, 0.0f, NoLoads{});
+            scores<DT, VT, DP, false, false>(s, q, keys, s, x, r.sum, c, 0.0f, NoLoads{});
             if (more) {
                 if ((t + 1) % S::kBatch == 0) st.find_pages(t + 1);
                 wait_lds();
@@ -931,8 +939,8 @@ struct KeyWalk {
             }
             const bool whole = key0 >= plain_lo && key0 <= plain_hi && there == 3;
             if (!whole) hide(s, lo - key0, hi - key0, there);
-            move_top<VT, DP>(r, s, largest(s), c);
-            exponentials<VT>(s, x, r.sum, c, r.base, 0, 16);
+            move_top<VT, DP, false>(r, s, largest(s), c);
+            exponentials<VT, false>(s, x, r.sum, c, r.base, 0, 16);
             if constexpr (S::kDirect) {
                 if (more) wait_loads<S::kLoads>();
                 else wait_loads<0>();

@@ -250,7 +250,7 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint32_t at)
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                  :
                  : "v"(from), "s"(at)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // The same from a uniform base and a lane's byte offset.
@@ -259,7 +259,7 @@ __device__ __forceinline__ void load_to_lds(const void *base, uint32_t offset, u
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
                  :
                  : "s"(base), "v"(offset), "s"(at)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 __device__ __forceinline__ uint32_t lds_address(const char *p)

@@ -296,26 +296,28 @@ def _on_device(call):
     return run
 
 
-def _wants_gradient(*tensors):
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if isinstance(t, torch.Tensor) and t.requires_grad:
-                return True
+_grad_enabled = torch.is_grad_enabled
+_count_version = torch.autograd.graph.increment_version
+
+
+def _wants_gradient(tensors):
+    for t in tensors:
+        if t is not None and getattr(t, "requires_grad", False):
+            return True                 # what is no tensor is refused further on
     return False
 
 
-def _no_gradient(call, why, *tensors):
+def _no_gradient(call, why):
     # A call without a gradient must not cut a graph in silence.
-    if _wants_gradient(*tensors):
-        raise RuntimeError(f"{call}: {why}; call it under torch.no_grad() or detach its arguments")
+    raise RuntimeError(f"{call}: {why}; call it under torch.no_grad() or detach its arguments")
 
 
-def _written(*tensors):
+def _written(*given):
     # Tells autograd that the caller's tensors were written in place (None: a
     # new one was made), so that it notices where it had kept one.
-    given = [t for t in tensors if t is not None]
+    given = [t for t in given if t is not None]
     if given:
-        torch.autograd.graph.increment_version(given)
+        _count_version(given)
 
 
 def _raw_stream(t):
@@ -387,7 +389,7 @@ def bevpool_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     derivative.  Where a gradient is wanted the outputs are new tensors, and
     the call is not captured in a graph: capture it under torch.no_grad() and
     bevpool_qk_norm_rope_backward after it."""
-    if _wants_gradient(q, k, q_weight, k_weight, q_out, k_out):
+    if _grad_enabled() and _wants_gradient((q, k, q_weight, k_weight, q_out, k_out)):
         if q_out is not None or k_out is not None:
             raise RuntimeError("bevpool_qk_norm_rope: q_out and k_out are not differentiable; leave "
                                "them out or call it under torch.no_grad()")
@@ -448,8 +450,8 @@ def bevpool_qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: Optional[torch.T
     bevpool_qk_norm_rope_backward_workspace_size bytes; made here when None.
     Keyword stream: where to run.  The gradients carry no graph; one that is
     asked for (dq_out or dk_out with requires_grad) is refused."""
-    _no_gradient("bevpool_qk_norm_rope_backward", "there is no second derivative", dq_out, dk_out,
-                 dq, dk)
+    if _grad_enabled() and _wants_gradient((dq_out, dk_out, dq, dk)):
+        _no_gradient("bevpool_qk_norm_rope_backward", "there is no second derivative")
     lib = _lib()
     given = dq, dk
     _token_rows("dq_out", dq_out)
@@ -504,8 +506,8 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
     or bfloat16.  Rows of q_out outside every sequence are left as they were.
     Keyword stream: where to run.  It has no gradient: arguments with
     requires_grad are refused where gradients are on."""
-    _no_gradient("bevpool_kv_append", "it has no gradient", k, v, q, q_weight, k_weight, q_out,
-                 cache.k, cache.v)
+    if _grad_enabled() and _wants_gradient((k, v, q, q_weight, k_weight, q_out, cache.k, cache.v)):
+        _no_gradient("bevpool_kv_append", "it has no gradient")
     lib = _lib()
     given = q_out
     sk = _token_rows("k", k)
@@ -556,7 +558,8 @@ def bevpool_paged_attention(q: torch.Tensor, cache: PagedCache, batch: PagedBatc
     calls that may overlap in time need one each.  Keyword stream: where to
     run.  It has no gradient: arguments with requires_grad are refused where
     gradients are on."""
-    _no_gradient("bevpool_paged_attention", "it has no gradient", q, out, cache.k, cache.v)
+    if _grad_enabled() and _wants_gradient((q, out, cache.k, cache.v)):
+        _no_gradient("bevpool_paged_attention", "it has no gradient")
     lib = _lib()
     sq = _token_rows("q", q)
     n, hq, dim = q.shape

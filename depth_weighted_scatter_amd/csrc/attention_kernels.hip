@@ -22,15 +22,17 @@
 // their registers.
 //
 // What bounds it.  Single tokens read each key and value once: 64 requests of
-// up to 8192 keys (32 heads on 8, 128 dims, bf16) 246 us, 5.6 TB/s; two of
-// 131072 (e4m3) 46 us and 7 for the join.  Chunks are bound by issue: for 64
+// up to 8192 keys (32 heads on 8, 128 dims, bf16) 245 us, 5.6 TB/s; two of
+// 131072 (e4m3) 47 us and 7 for the join.  Chunks are bound by issue: for 64
 // keys of 128 dims a wave has 32 matrix instructions (1024 cycles of the
-// matrix cores), 32 exponentials and some 300 other instructions, and the two
-// waves of a SIMD take 4100 cycles for theirs.  4096 tokens after 8192 cached
-// ones (32 heads on 8) take 665 to 710 us, 1.0 PFLOP/s, at the clock that
-// power leaves; the library's large product reaches 1.18.  A block takes
-// about 14000 cycles to begin (its place, its queries, its first keys) and
-// 12000 to end; over 2816 keys (704 tokens, 80 dims: 77 us) that is a third.
+// matrix cores), 32 exponentials and some 200 other vector instructions, and
+// the two waves of a SIMD take about 4200 cycles for theirs: the matrix cores
+// are busy 46 % of the time.  4096 tokens after 8192 cached ones (32 heads on 8)
+// take 670 to 700 us in a row, 0.98 to 1.03 PFLOP/s, and 730 to 840 in a
+// profiler's pauses, at the clock that power leaves (2.3 GHz falling to 1.7);
+// the library's large product reaches 1.18.  A block takes about 13 us to begin
+// (its place, its queries, its first keys) and end: a sixth of 6 x 704 tokens
+// over 2816 keys (80 dims, 77 to 86 us), which keep 144 of the 256 CUs.
 #include <hip/hip_runtime.h>
 
 #include "token_device.h"
@@ -571,8 +573,8 @@ __device__ __forceinline__ float both_halves(float x)
 // differences to the reference first.  Where instructions are not what bounds a
 // walk, or a second path costs it registers, every weight takes the difference
 // (64 single tokens of up to 8192 keys 249 us with ONE, 244 without; 2 x 1024
-// tokens over 4096 keys, 16 heads of 256 on 4, bf16 297 and 240, e4m3 371 and
-// 379).
+// tokens after 3072 cached ones, 16 heads of 256 on 4, bf16 297 and 240, e4m3
+// 371 and 379).
 constexpr float kFar = 4096.0f;
 
 // Takes the largest of a lane's scores s into the running maximum.  The

@@ -1,11 +1,14 @@
 // Norm and rotation of query and key heads, its gradient, and the append to a
 // paged cache (gfx950).  See bevpool.h for the formulas.
 //
-// All three are one pass over their rows and bound by HBM: about ten
-// operations for each element read and written.  What decides the time is
-// that every load is 16 bytes wide, that a pair's two coordinates meet in one
-// lane, and that the angle (fp64 product, reduction, sine and cosine: some 60
-// instructions) is paid once per token and pair, not once per head.
+// All three are one pass over their rows and bound by HBM where they are
+// large: about ten operations for each element read and written.  What decides
+// the time is that every load is 16 bytes wide, that a pair's two coordinates
+// meet in one lane, and that the angle (fp64 product, reduction, sine and
+// cosine: some 60 instructions) is paid once for a token, a pair and a chunk of
+// heads.  With few tokens the heads are dealt to more waves, and each works its
+// angles out again: 4 times at 16384 tokens of 20 heads, once a head at 4223
+// tokens of 10.  So do the append's waves that hold values alone.
 //
 // Layout.  A row of head_dim elements belongs to LPR lanes (the power of two
 // at or above head_dim / 16), each lane holding two runs of eight elements:
@@ -16,10 +19,12 @@
 // keeping its eight sines and cosines.
 //
 // Measured (a 2 GiB copy moves 4.96 TB/s): 16384 tokens of 16 + 4 heads of 128,
-// bf16: forward 41 us (4.1 TB/s), backward 53 us (4.7) and 4 for the last sum of
-// the weight gradient.  Append of 16384 tokens, 16 query heads, 8 key heads of
-// 128, bf16 to e4m3: 49 us (4.8 TB/s), of 64 single tokens 6 us: the chain
-// offsets, place, page, store.
+// bf16: forward 42 us (4.0 TB/s), backward 54 us (4.7) and 4.6 for the last sum
+// of the weight gradient.  Append of 16384 tokens, 16 query heads, 8 key heads
+// of 128, bf16 to e4m3: 50 us (4.7 TB/s), of 64 single tokens 6 us: the chain
+// offsets, place, page, store.  4223 tokens of 5 + 5 heads of 80, fp32: forward
+// 12 us and backward 15 + 4, 2.2 times their bytes: the angles of every head,
+// and 3 of 8 lanes without elements.
 #include <hip/hip_runtime.h>
 
 #include "token_device.h"
@@ -49,8 +54,10 @@ __device__ __forceinline__ Slot slot_of(int j, int head_dim, int half, bool adja
 
 // Cosines and sines of the lane's eight angles.  position * inv_freq has up
 // to 55 significant bits and is rounded to fp64's 53; the turn's fraction
-// then keeps an absolute error of 2^-53 of the number of turns, so a token
-// two million radians out still has its angle to 2^-30.
+// then keeps an absolute error of 2^-53 of the number of turns: two million
+// radians out the reduction is right to 2^-30.  Its result is rounded to fp32,
+// so at any position the angle that the sine is taken of is right to about
+// 2^-23 radians (2^-25 half turns), and no better.
 __device__ __forceinline__ void angles(const RopeParams &p, const Slot &s, int token, f32x8 &cs,
                                        f32x8 &sn)
 {
@@ -404,9 +411,10 @@ __global__ __launch_bounds__(kBlock) void append(AppendParams a, int chunk)
                                              g.v_scale, to(g.v_cache));
 }
 
-// Heads of one unit of work: enough units for about eight waves on each of
-// the 1,024 SIMDs when there are few tokens, all heads of a token in one
-// unit (its angles computed once) when there are many.
+// Heads of one unit of work: enough units for about eight waves for each of
+// the 1,024 SIMDs when there are few tokens (six run at once, three to four of
+// the gradient's), all heads of a token in one unit (its angles computed once)
+// when there are many.
 int head_chunk(int64_t token_waves, int heads)
 {
     const int64_t want = 8192 / (token_waves > 0 ? token_waves : 1);

@@ -430,6 +430,8 @@ def _qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, q_out, k_out):
 
 def bevpool_qk_norm_rope_backward_workspace_size(n_tokens: int, n_q_heads: int, n_k_heads: int,
                                                  head_dim: int) -> int:
+    """Bytes of workspace of bevpool_qk_norm_rope_backward.  Fewer tokens may
+    need more: a buffer for several sizes has the largest of theirs."""
     return _lib().bevpool_qk_norm_rope_backward_workspace_size(n_tokens, n_q_heads, n_k_heads,
                                                                head_dim)
 
@@ -541,6 +543,8 @@ def bevpool_kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedCache, batch
 def bevpool_paged_attention_workspace_size(n_tokens: int, n_seqs: int, n_q_heads: int,
                                            n_k_heads: int, head_dim: int, page_size: int,
                                            max_pages: int) -> int:
+    """Bytes of workspace of bevpool_paged_attention.  A smaller batch may need
+    more: a buffer for several batches has the largest of their sizes."""
     return _lib().bevpool_paged_attention_workspace_size(n_tokens, n_seqs, n_q_heads, n_k_heads,
                                                          head_dim, page_size, max_pages)
 

@@ -366,7 +366,8 @@ int bevpool_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t
                          int64_t k_out_stride, hipStream_t stream);
 
 /* Bytes of device workspace bevpool_qk_norm_rope_backward needs (0 for
- * invalid sizes). */
+ * invalid sizes).  Fewer tokens may need more, as heads are then dealt to more
+ * waves: one buffer for several sizes has the largest of theirs. */
 size_t bevpool_qk_norm_rope_backward_workspace_size(int64_t n_tokens, int32_t n_q_heads,
                                                     int32_t n_k_heads, int32_t head_dim);
 
@@ -454,7 +455,12 @@ int bevpool_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_
 
 /*
  * Bytes of device workspace bevpool_paged_attention needs for these sizes (0
- * for invalid ones; never 0 for valid ones).
+ * for invalid ones; never 0 for valid ones).  They do not grow with the batch:
+ * fewer tokens or sequences may need more, since the keys of fewer tiles are
+ * cut into more parts.  A program that keeps one buffer takes the largest over
+ * the batches that it will run.  The cut follows from these sizes, not from the
+ * lengths: a table much wider than its sequences, or one sequence much longer
+ * than the others, costs time.
  */
 size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
                                               int32_t n_q_heads, int32_t n_k_heads,
@@ -471,11 +477,11 @@ size_t bevpool_paged_attention_workspace_size(int64_t n_tokens, int32_t n_seqs,
  * place of token t, satisfy j <= p if causal and j > p - window if window > 0.
  * A token that sees no key gets 0; a score of -infinity has weight 0, also
  * where there are no others.  Keys and values in hidden places have no
- * influence, infinities and NaN among them.  A coordinate of an output is
- * finite exactly if that coordinate of every value the token sees is, whatever
- * their weights; whether it is infinite or NaN otherwise is not specified (a
- * weight that rounds to 0 may make NaN of an infinity).  Chunks, single tokens,
- * or both in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
+ * influence, infinities and NaN among them.  With finite scores, and sums
+ * within fp32, a coordinate of an output is finite exactly if that coordinate
+ * of every value the token sees is, whatever their weights; whether it is
+ * infinite or NaN otherwise is not specified (a weight that rounds to 0 may
+ * make NaN of an infinity).  Chunks, single tokens, or both in one batch.  n_q_heads is a multiple of n_k_heads.  Scores, softmax
  * statistics and sums are fp32; the weights enter the product with v rounded
  * to BF16 for a BF16 cache and to F16 for the others, the sum they are divided
  * by takes them unrounded (F16 weights below 2^-32 of the largest count as 0).

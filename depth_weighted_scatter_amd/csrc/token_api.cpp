@@ -212,7 +212,8 @@ int bevpool_qk_norm_rope_backward(const void *dq_out, int64_t dq_out_stride, con
                         weight_dtype, eps, positions, n_axes, h_sections, inv_freq, layout, p);
     if (st != BEVPOOL_OK) return st;
     if (n_q_heads <= 0) return BEVPOOL_ERR_INVALID_ARG;
-    if (n_k_heads == 0) p.k_weight = nullptr;
+    // no key heads: a given gradient of their weight becomes zeros
+    if (n_k_heads == 0 && !dk_weight) p.k_weight = nullptr;
     if ((p.q_weight && (!dq_weight || !aligned(dq_weight, 4))) ||
         (p.k_weight && (!dk_weight || !aligned(dk_weight, 4))))
         return BEVPOOL_ERR_INVALID_ARG;

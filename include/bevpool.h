@@ -385,7 +385,7 @@ size_t bevpool_qk_norm_rope_backward_workspace_size(int64_t n_tokens, int32_t n_
  *   dq, dk: gradients of q and k (dtype); each may be dq_out / dk_out itself
  *       (same pointer and stride).
  *   dq_weight, dk_weight [head_dim] fp32, overwritten; required with their
- *       weight, ignored without.
+ *       weight (dk_weight may be NULL without key heads), ignored without.
  *   workspace: at least bevpool_qk_norm_rope_backward_workspace_size() bytes,
  *       256-byte aligned; contents on entry are ignored.
  * Everything else as bevpool_qk_norm_rope.  Errors: also WORKSPACE.

@@ -172,7 +172,7 @@ def _token_rows(name, t, like=None):
         if t.get_device() != like.get_device():
             raise ValueError(f"{name} lies on another device")
     st, sh, sd = t.stride()
-    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+    if ((sd != 1 and dim > 1) or (sh != dim and heads > 1)) and n > 0:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st if n > 1 else heads * dim
 

@@ -10,7 +10,7 @@ from token_util import make_rope, values
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("n", [0, 1, 70])
 def test_keys_of_no_heads(n):
     rng = np.random.default_rng(151)
     pos, _, f, _ = make_rope(rng, (16,), n)

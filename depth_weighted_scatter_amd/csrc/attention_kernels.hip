@@ -572,9 +572,9 @@ __device__ __forceinline__ float both_halves(float x)
 // powers of two, and past 2^31 by all that fp32 holds: there the scores become
 // differences to the reference first.  Where instructions are not what bounds a
 // walk, or a second path costs it registers, every weight takes the difference
-// (64 single tokens of up to 8192 keys 249 us with ONE, 244 without; 2 x 1024
-// tokens after 3072 cached ones, 16 heads of 256 on 4, bf16 297 and 240, e4m3
-// 371 and 379).
+// (64 single tokens of up to 8192 keys 249 us with ONE, 244 without; the last
+// 1024 tokens of 2 x 4096, 16 heads of 256 on 4, bf16 297 and 240, e4m3 371 and
+// 379).
 constexpr float kFar = 4096.0f;
 
 // Takes the largest of a lane's scores s into the running maximum.  The

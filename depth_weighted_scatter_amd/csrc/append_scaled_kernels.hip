@@ -22,6 +22,7 @@
 // the bottom of the format.
 #include <hip/hip_runtime.h>
 
+#include "append_walk.h"
 #include "rope_device.h"
 
 namespace bevpool {
@@ -30,17 +31,6 @@ namespace {
 constexpr int kMostThreads = 1024, kHeadThreads = 64;
 constexpr int kChipThreads = 256 * 1024;      // four waves of append_blocks a SIMD
 constexpr float kMostCode = 448.0f;
-
-// Tiles of the launch, a block of tokens each: sequence s has those from
-// off(s) / tokens + PER s on, and so at least n / tokens + PER for its n new
-// tokens, which lie in at most n / tokens + 2 blocks.  With PER = 1 the last tile
-// takes what is left; with 2 there is none left (and half of the tiles of
-// sequences of few tokens are nobody's).
-template <int PER>
-__device__ __forceinline__ int64_t first_tile(int64_t off, int seq, int block_shift)
-{
-    return (off >> block_shift) + PER * int64_t(seq);
-}
 
 // Cosines and sines of the lane's eight angles: the turns in fp64, as far positions
 // need them, their fraction by the hardware's sine, which takes turns and is within
@@ -166,46 +156,15 @@ __device__ __forceinline__ f32x8 floats(u32x4 x)
     return __builtin_convertvector(__builtin_bit_cast(V, x), f32x8);
 }
 
-// New tokens of one block.
-struct Piece {
-    int64_t token0;       // first of them
-    int64_t row0;         // the block's first slot, in rows of head 0
-    int count, early;     // new tokens; places before them in the block
-    bool kept;            // the block is on a page
-};
-
 // Calls f(Piece) for the new tokens of a tile.
 template <int PER, typename F>
 __device__ __forceinline__ void each_piece(const AppendParams &a, int64_t tile, F f)
 {
-    const RopeParams &p = a.rope;
     const PagedParams &g = a.paged;
-    const int shift = g.block_shift;
-    const auto off = [&](int i) { return int64_t(clip(g.q_offsets[i], 0, p.n_tokens)); };
-    const int seq = count_upto(g.n_seqs, tile, [&](int i) { return first_tile<PER>(off(i), i, shift); });
-    if (seq >= g.n_seqs) return;
-    const int64_t begin = off(seq), end = off(seq + 1);
-    if (begin >= end) return;
-    const int64_t place0 = int64_t(g.kv_lengths[seq]) - g.q_offsets[seq + 1] + begin;
-    const int64_t place_end = place0 + end - begin;
-    int64_t block = (place0 >> shift) + tile - first_tile<PER>(begin, seq, shift);
-    const int64_t block_end = ((place_end - 1) >> shift) + 1;
-    const bool last_tile = tile + 1 == first_tile<PER>(end, seq + 1, shift);
-    for (; block < block_end; ++block) {
-        const int64_t lo = max(place0, block << shift), hi = min(place_end, (block + 1) << shift);
-        Piece c;
-        c.count = int(hi - lo);
-        c.early = int(lo - (block << shift));
-        c.token0 = begin + lo - place0;
-        int page = -1;
-        if (lo >= 0 && lo < int64_t(g.max_pages) << g.page_shift)
-            page = g.block_table[int64_t(seq) * g.max_pages + (lo >> g.page_shift)];
-        c.kept = page >= 0 && page < g.n_pages;
-        c.row0 = ((int64_t(c.kept ? page : 0) * p.n_k_heads) << g.page_shift) +
-                 ((lo - c.early) & ((1 << g.page_shift) - 1));
-        f(c);
-        if (PER == 2 || !last_tile) return;
-    }
+    const int seq = count_upto(g.n_seqs, tile, [&](int i) {
+        return first_tile<PER>(token_offset(a, i), i, g.block_shift);
+    });
+    if (seq < g.n_seqs) pieces_of<PER>(a, seq, tile, f);
 }
 
 template <int LPR>

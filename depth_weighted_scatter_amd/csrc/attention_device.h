@@ -1496,6 +1496,22 @@ Shape shape_of(int64_t n_tokens, int32_t n_seqs, int32_t n_q_heads, int32_t n_k_
     return s;
 }
 
+// Blocks that join the splits of a tile.  A block's begin costs what some 30 rows do,
+// so where tiles fill the chip by themselves it takes 64 rows (6 x 704 rows of 80 in 3
+// splits over 4224 keys: 64 rows a block 113.6 us, 32 114.9, 16 121.9); tiles that are
+// few have up to 16 blocks each, or the join would take a handful of CUs.  With 64 rows
+// a block and with these (us): a token of 64 heads on one over 131072 keys, 57 splits
+// 71 and 49; 256 tokens over 8192, 8 heads on 2, 11 splits 46 and 34; 16 over 32768, 32
+// on 8, 26 splits 48 and 38; over scales of blocks 57 and 38, 51 and 38, 42 and 34.
+// Tiles of few rows and few splits are done by one block (320 tiles, 2 splits: 241 us
+// against 249), those of many splits by four (3 x 32 rows in 21: 80 us, 83 with one).
+inline uint32_t join_blocks(const Shape &s, int64_t rows, int32_t n_seqs, int32_t n_k_heads)
+{
+    if (rows <= int64_t(n_seqs) * n_k_heads * kRowsPerWave) return s.splits < 16 ? 1 : 4;
+    const int64_t least = (s.tile_rows + 63) / 64, fill = 256 / (s.tiles * n_k_heads);
+    return uint32_t(fill < least ? least : fill < 16 ? fill : 16);
+}
+
 inline size_t round_up(size_t n) { return (n + 255) & ~size_t(255); }
 
 inline size_t workspace_of(const Shape &s, int64_t n_tokens, int32_t n_q_heads, int32_t head_dim)
@@ -1543,14 +1559,7 @@ hipError_t attention(const AttnParams &p, hipStream_t stream)
     launch_attend<DT, CDT>(p, parts, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.splits == 1) return e;
-    // 64 rows a block, as its begin costs what some 30 rows do (6 x 704 rows of 80 in 3
-    // splits: 8 rows 141 us, 16 124, 32 116.5, 64 115.5, 128 116.3),
-    // and four blocks for a tile of few rows and many splits (3 x 32 rows in 21: 80 us,
-    // 83 with one); tiles of few rows and few splits are done by one (320 tiles, 2
-    // splits: 241 us against 249)
-    const bool few = parts.rows <= int64_t(p.paged.n_seqs) * p.n_k_heads * kRowsPerWave;
-    const dim3 blocks(uint32_t(s.tiles * p.n_k_heads),
-                      few ? (s.splits < 16 ? 1 : 4) : uint32_t((s.tile_rows + 63) / 64));
+    const dim3 blocks(uint32_t(s.tiles * p.n_k_heads), join_blocks(s, parts.rows, p.paged.n_seqs, p.n_k_heads));
     attend_join<DT, CDT><<<blocks, kJoinBlock, 0, stream>>>(p, parts, s.tile_rows, s.splits);
     return hipGetLastError();
 }

@@ -9,7 +9,8 @@
 // bring many (append_blocks) a block of threads holds a block of tokens and walks
 // over heads, the waves' largest meeting in LDS, one barrier a head.  1024 threads
 // hold 1024 / lanes-per-row tokens at once; wider blocks (256 tokens of 128 dims,
-// 128 of 256) are held in two strips, 256 of 256 in four that are read twice.
+// 128 of 256) are held in two strips, 256 of 256 in four that are read twice.  Their
+// angles lie in LDS, so that no register is spilled.
 //
 // Bound by HBM where large: 16384 tokens of 16 on 8 heads of 128 (bf16, 235 MB)
 // 56 us, 4.2 TB/s; what is left to the copy's rate is the begin of each share (offsets,
@@ -32,16 +33,12 @@ constexpr int kMostThreads = 1024, kHeadThreads = 64;
 constexpr int kChipThreads = 256 * 1024;      // four waves of append_blocks a SIMD
 constexpr float kMostCode = 448.0f;
 
-// Cosines and sines of the lane's eight angles: the turns in fp64, as far positions
-// need them, their fraction by the hardware's sine, which takes turns and is within
-// 2^-22.9 (measured over 2^24 angles; sincospif 2^-24.2, but 40 instructions where
-// this is one: 19 prompts of up to 1703 tokens, 10 on 5 heads of 80, 28.0 us with
-// that and 26.8 with this).  What comes of it is rounded to 16 bits or to a code.
-__device__ __forceinline__ void turns(const RopeParams &p, const Slot &s, int token, f32x8 &cs, f32x8 &sn)
+// The lane's eight angles, in turns from -1/2 to 1/2: formed in fp64, as far positions
+// need them.
+__device__ __forceinline__ f32x8 fractions(const RopeParams &p, const Slot &s, int token)
 {
-    cs = 1.0f;
-    sn = 0.0f;
-    if (s.pair < 0) return;
+    f32x8 part = 0.0f;
+    if (s.pair < 0) return part;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int pair = s.pair + i;
@@ -50,10 +47,52 @@ __device__ __forceinline__ void turns(const RopeParams &p, const Slot &s, int to
         for (int a = 0; a < kMaxRopeAxes - 1; ++a)
             if (a + 1 < p.n_axes && pair >= p.section_end[a]) axis = a + 1;
         const double angle = double(p.positions[int64_t(axis) * p.n_tokens + token]) * double(p.inv_freq[pair]);
-        const double t = angle * 0.15915494309189533577;       // 1 / (2 pi)
-        const float part = float(t - rint(t));
-        cs[i] = __builtin_amdgcn_cosf(part);
-        sn[i] = __builtin_amdgcn_sinf(part);
+        const double per_turn = 0.15915494309189533577;        // 1 / (2 pi)
+        part[i] = float(fma(angle, per_turn, -rint(angle * per_turn)));
+    }
+    return part;
+}
+
+// Cosines and sines of four of them, by the hardware's sine, which takes turns and is within
+// 2^-22.9 (measured over 2^24 angles; sincospif 2^-24.2, but 40 instructions where
+// this is one: 19 prompts of up to 1703 tokens, 10 on 5 heads of 80, 28.0 us with
+// that and 26.8 with this).  What comes of it is rounded to 16 bits or to a code.
+struct Turn4 { f32x4 cs, sn; };
+
+__device__ __forceinline__ Turn4 turns_of(f32x4 part)
+{
+    Turn4 t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t.cs[i] = __builtin_amdgcn_cosf(part[i]);
+        t.sn[i] = __builtin_amdgcn_sinf(part[i]);
+    }
+    return t;
+}
+
+__device__ __forceinline__ f32x4 low(f32x8 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3); }
+__device__ __forceinline__ f32x4 high(f32x8 v) { return __builtin_shufflevector(v, v, 4, 5, 6, 7); }
+__device__ __forceinline__ f32x8 both(f32x4 a, f32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// Turns the lane's pairs 0 to 3, or 4 to 7.
+template <bool ADJ, int HALF>
+__device__ __forceinline__ void rotate4(f32x8 &a, f32x8 &b, const Turn4 &t)
+{
+    f32x8 &own = HALF ? b : a;
+    f32x4 u, v;
+    if constexpr (ADJ) {
+        u = __builtin_shufflevector(own, own, 0, 2, 4, 6);
+        v = __builtin_shufflevector(own, own, 1, 3, 5, 7);
+    } else {
+        u = HALF ? high(a) : low(a);
+        v = HALF ? high(b) : low(b);
+    }
+    const f32x4 x = u * t.cs - v * t.sn, y = v * t.cs + u * t.sn;
+    if constexpr (ADJ) {
+        own = __builtin_shufflevector(x, y, 0, 4, 1, 5, 2, 6, 3, 7);
+    } else {
+        a = HALF ? both(low(a), x) : both(x, high(a));
+        b = HALF ? both(low(b), y) : both(y, high(b));
     }
 }
 
@@ -210,16 +249,18 @@ __global__ __launch_bounds__(kHeadThreads) void append_heads(AppendParams a, int
             const bool on = s.on && there && t < c.count;
             t = min(t, c.count - 1);
             const Raw raw = load_raw<DT>(src + (c.token0 + t) * stride, s, on);
-            f32x8 wa, wb, cs, sn;
+            f32x8 wa, wb;
             load_weight<DT>(p, weight, s, wa, wb);
-            turns(p, s, int(c.token0 + t), cs, sn);
+            const f32x8 part = fractions(p, s, int(c.token0 + t));
             x = floats<DT>(raw.a);
             y = floats<DT>(raw.b);
             f32x8 u = x, v = y;
             normed<LPR>(u, v, wa, wb, inv_dim, p.eps);      // by all lanes: it sums over them
             x = weight ? u : x;
             y = weight ? v : y;
-            rotate<ADJ>(x, y, cs, sn, s.pair >= 0 && (is_q || is_k));
+            if (s.pair < 0 || !(is_q || is_k)) return;
+            rotate4<ADJ, 0>(x, y, turns_of(low(part)));
+            rotate4<ADJ, 1>(x, y, turns_of(high(part)));
         };
         const float old = stored && c.early > 0 ? block_scale(*at) : 0.0f;
         float most = 0.0f;
@@ -268,6 +309,10 @@ __global__ __launch_bounds__(kMostThreads) void append_blocks(AppendParams a, in
     constexpr bool kAhead = STRIPS == 1;            // registers for more are not there
     constexpr int kHeld = kHold ? STRIPS : 1;
     __shared__ float wave_most[2][kMostThreads / kLanes];
+    // Of several strips' angles: two strips' sines and cosines, four strips' turns; a
+    // thread reads what it wrote.
+    constexpr int kPieces = STRIPS == 1 ? 0 : 8 / STRIPS;
+    __shared__ f32x4 angles_of[STRIPS == 1 ? 1 : 8 * kMostThreads];
     const RopeParams &p = a.rope;
     const PagedParams &g = a.paged;
     const int tid = int(threadIdx.x), lane = tid & (kLanes - 1);
@@ -289,14 +334,39 @@ __global__ __launch_bounds__(kMostThreads) void append_blocks(AppendParams a, in
             const int waves = (min(c.count, rows) * LPR + kLanes - 1) / kLanes;     // that have rows
             const auto index = [&](int st) { return st * rows + tid / LPR; };
             const auto on = [&](int st) { return s.on && index(st) < c.count; };
-            const auto token = [&](int st) { return c.token0 + min(index(st), c.count - 1); };
+            const auto token = [&](int st) { return c.token0 + index(st); };        // where on(st)
             const auto used = [&](int st) { return st == 0 || st * rows < c.count; };
-            f32x8 cs[STRIPS], sn[STRIPS], wa, wb;
+            Turn4 held[2];
+            f32x8 wa, wb;
+            const auto piece = [&](int st, int n) -> f32x4 & {
+                return angles_of[(st * kPieces + n) * kMostThreads + tid];
+            };
             if (h0 < nq + nk) {
+                for (int st = 0; st < STRIPS; ++st) {
+                    if (!used(st)) continue;
+                    const f32x8 part = fractions(p, s, int(c.token0) + min(index(st), c.count - 1));
+                    if constexpr (STRIPS == 4) {
+                        piece(st, 0) = low(part);
+                        piece(st, 1) = high(part);
+                    } else {
 #pragma unroll
-                for (int st = 0; st < STRIPS; ++st)
-                    if (used(st)) turns(p, s, int(token(st)), cs[st], sn[st]);
+                        for (int n = 0; n < 2; ++n) {
+                            const Turn4 t = turns_of(n ? high(part) : low(part));
+                            if constexpr (STRIPS == 1) {
+                                held[n] = t;
+                            } else {
+                                piece(st, 2 * n) = t.cs;
+                                piece(st, 2 * n + 1) = t.sn;
+                            }
+                        }
+                    }
+                }
             }
+            const auto turn4 = [&](int st, int n) {
+                if constexpr (STRIPS == 1) return held[n];
+                else if constexpr (STRIPS == 2) return Turn4{piece(st, 2 * n), piece(st, 2 * n + 1)};
+                else return turns_of(piece(st, n));
+            };
             // Heads [from, to) of one kind, each as fetched, normed and turned.
             Raw next;
             const auto fetch = [&](const void *src, int64_t stride, int h, int st) {
@@ -306,7 +376,9 @@ __global__ __launch_bounds__(kMostThreads) void append_blocks(AppendParams a, in
                 x = floats<DT>(raw.a);
                 y = floats<DT>(raw.b);
                 if (norm) normed<LPR>(x, y, wa, wb, inv_dim, p.eps);
-                if (turn) rotate<ADJ>(x, y, cs[st], sn[st], s.pair >= 0);
+                if (!turn || s.pair < 0) return;
+                rotate4<ADJ, 0>(x, y, turn4(st, 0));
+                rotate4<ADJ, 1>(x, y, turn4(st, 1));
             };
 
             if (h0 < nq && (waves > 1 || wave == 0)) {

@@ -7,6 +7,7 @@ import re
 
 import pytest
 
+from codegen_util import saved_before_restore
 from test_tokens_codegen import HIPCC, _compile
 
 # attend<DT, e4m3 with scales of blocks, DP, EXACT>: most scratch (bytes a lane), by (DP, EXACT)
@@ -64,3 +65,17 @@ def test_attention_kernels(codegen):
 def test_no_packed_fp32(codegen, name):
     asm, _ = codegen[name]
     assert not re.search(r"v_pk_(add|mul|fma)_f32", asm)
+
+
+def test_append_keeps_its_registers(codegen):
+    """No append spills: one whose angles were spilled lost them for lanes that a
+    missing weight had switched off."""
+    _, usage = codegen["append_scaled"]
+    assert len(usage) == 52
+    for k, u in usage.items():
+        assert u["ScratchSize"] == 0, f"{k}: {u}"
+
+
+@pytest.mark.parametrize("name", ["append_scaled", "assign", "attention_scaled"])
+def test_saves_have_all_lanes(codegen, name):
+    assert saved_before_restore(codegen[name][0]) == []

@@ -16,6 +16,8 @@ import subprocess
 
 import pytest
 
+from codegen_util import saved_before_restore
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "depth_weighted_scatter_amd", "csrc")
 HIPCC = "/opt/rocm/bin/hipcc"
@@ -84,3 +86,8 @@ def test_attention_kernels(codegen):
 def test_no_packed_fp32(codegen, name):
     asm, _ = codegen[name]
     assert not re.search(r"v_pk_(add|mul|fma)_f32", asm)
+
+
+@pytest.mark.parametrize("name", ["rope", "attention"])
+def test_saves_have_all_lanes(codegen, name):
+    assert saved_before_restore(codegen[name][0]) == []

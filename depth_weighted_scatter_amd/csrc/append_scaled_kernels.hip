@@ -74,7 +74,9 @@ __device__ __forceinline__ f32x4 low(f32x8 v) { return __builtin_shufflevector(v
 __device__ __forceinline__ f32x4 high(f32x8 v) { return __builtin_shufflevector(v, v, 4, 5, 6, 7); }
 __device__ __forceinline__ f32x8 both(f32x4 a, f32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-// Turns the lane's pairs 0 to 3, or 4 to 7.
+// Turns the lane's pairs 0 to 3, or 4 to 7.  Which product a sum takes unrounded is
+// written out, here and in the norm: left to the compiler it differed between the
+// kernels, and with it a bit of the result between launches.
 template <bool ADJ, int HALF>
 __device__ __forceinline__ void rotate4(f32x8 &a, f32x8 &b, const Turn4 &t)
 {
@@ -87,7 +89,7 @@ __device__ __forceinline__ void rotate4(f32x8 &a, f32x8 &b, const Turn4 &t)
         u = HALF ? high(a) : low(a);
         v = HALF ? high(b) : low(b);
     }
-    const f32x4 x = u * t.cs - v * t.sn, y = v * t.cs + u * t.sn;
+    const f32x4 x = __builtin_elementwise_fma(u, t.cs, -(v * t.sn)), y = __builtin_elementwise_fma(u, t.sn, v * t.cs);
     if constexpr (ADJ) {
         own = __builtin_shufflevector(x, y, 0, 4, 1, 5, 2, 6, 3, 7);
     } else {
@@ -209,8 +211,7 @@ __device__ __forceinline__ void each_piece(const AppendParams &a, int64_t tile, 
 template <int LPR>
 __device__ __forceinline__ void normed(f32x8 &x, f32x8 &y, f32x8 wa, f32x8 wb, float inv_dim, float eps)
 {
-    const float ms = row_sum<LPR>(dot8(x, x) + dot8(y, y)) * inv_dim;
-    const float r = 1.0f / sqrtf(ms + eps);
+    const float r = 1.0f / sqrtf(fmaf(row_sum<LPR>(dot8(x, x) + dot8(y, y)), inv_dim, eps));
     x = x * r * wa;
     y = y * r * wb;
 }

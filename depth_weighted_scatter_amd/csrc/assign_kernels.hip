@@ -18,6 +18,7 @@
 // prompts of up to 8191 tokens 3.1 + 5.3.
 #include <hip/hip_runtime.h>
 
+#include "assign_plan.h"
 #include "token_device.h"
 
 namespace bevpool {
@@ -30,13 +31,9 @@ constexpr int kWholeItems = 4096;     // tokens and pages that one block deals w
 using Seq = AssignSeq;
 using Step = AssignStep;
 
-struct Sums { uint32_t tokens, taken, returned; };
-
-// Tokens may pass 32 bits before the step is refused for it: they stop at 2^31 - 1.
-__device__ __forceinline__ Sums operator+(Sums a, Sums b)
-{
-    return {min(a.tokens + b.tokens, uint32_t(INT32_MAX)), a.taken + b.taken, a.returned + b.returned};
-}
+using Sums = AssignSums;
+using Lengths = AssignLengths;
+using Given = AssignGiven;
 
 // Another lane's, by a shift or broadcast within the vector pipe; 0 where CTRL names
 // none, or where ROWS leaves the lane out.
@@ -64,35 +61,9 @@ __device__ __forceinline__ Sums last_lane(Sums a)
     return {of(a.tokens), of(a.taken), of(a.returned)};
 }
 
-struct Lengths { int keep, fresh, before, after; bool fits; };
-
-// A sequence's three lengths as they are given.
-struct Given { int kv, keep, fresh; };
-
 __device__ __forceinline__ Given given_of(const AssignParams &p, int s)
 {
     return {p.kv_lengths[s], p.keep_lengths ? p.keep_lengths[s] : INT32_MAX, p.new_lengths[s]};
-}
-
-__device__ __forceinline__ Lengths lengths_of(const AssignParams &p, const Given &g)
-{
-    const int64_t room = int64_t(p.max_pages) << p.page_shift;
-    const int page = (1 << p.page_shift) - 1;
-    Lengths l;
-    l.fits = g.kv <= room;
-    const int kv = g.kv < 0 ? 0 : (l.fits ? g.kv : int(room));
-    l.keep = clip(g.keep, 0, kv);
-    l.fresh = max(g.fresh, 0);
-    l.fits = l.fits && l.keep + int64_t(l.fresh) <= room;
-    if (!l.fits) l.fresh = 0;                          // the step is refused
-    l.before = int((kv + int64_t(page)) >> p.page_shift);
-    l.after = int((l.keep + int64_t(l.fresh) + page) >> p.page_shift);
-    return l;
-}
-
-__device__ __forceinline__ Sums sums_of(const Lengths &l)
-{
-    return {uint32_t(l.fresh), uint32_t(max(l.after - l.before, 0)), uint32_t(max(l.before - l.after, 0))};
 }
 
 // The last of n non-decreasing values key(i) that is at most x, from key(0) <= x.
@@ -185,8 +156,9 @@ __device__ __forceinline__ void carry_out(const AssignParams &p, const Seq *seqs
                 p.block_table[int64_t(s) * p.max_pages + seqs[s].before + i - seqs[s].taken] =
                     taken_page(p, seqs, step, i);
         } else {
-            const int r = int(turn - to_entries) * kLanes + lane + step.taken;
-            if (r < step.returned) p.free_pages[step.count + step.returned - 1 - r] = returned_page(p, seqs, r);
+            const int64_t r = (turn - to_entries) * kLanes + lane + step.taken;
+            if (r < step.returned)
+                p.free_pages[int64_t(step.count) + step.returned - 1 - r] = returned_page(p, seqs, int(r));
         }
     }
 }
@@ -237,11 +209,9 @@ __global__ __launch_bounds__(kThreads) void plan_step(AssignParams p)
         if (w == wave) at = all;
         all = all + wave_sums[w];
     }
-    const int count = clip(listed, 0, p.n_free);
-    // the list has room for what comes back
-    const int64_t left = int64_t(count) + all.returned - all.taken;
-    const int status = bad || all.tokens > uint32_t(p.n_tokens) || left > p.n_free ? -1 : (left < 0 ? int(-left) : 0);
-    const Step step = {status, status ? 0 : int(all.taken), status ? 0 : int(all.returned), count};
+    int64_t left;
+    const Step step = step_of(p, all, !bad, listed, left);
+    const int status = step.refused;
     const auto write = [&](int s, const Given &g, Sums with) {
         const Lengths l = lengths_of(p, g);
         const Sums own = sums_of(l);       // of a step that is not refused no sum has stopped

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import depth_weighted_scatter_amd as dws
+from depth_weighted_scatter_amd import tokens
 from oracle import tokens as ref
 from token_util import dev
 
@@ -155,6 +156,31 @@ def test_totals_past_32_bits():
         p.count = count
         p.gpu()
         p.compare(p.step([40, 40, 40], None, 130), p.want([40, 40, 40], None, 130))
+
+
+def test_more_tokens_than_31_bits_hold():
+    """Room for 2^31 - 1 tokens, pages for all that are asked for, and 3 x 2^30 of
+    them: the step is refused (slots and places are not asked for)."""
+    n, page, width, listed = 3, 256, 2 ** 22, 3 * 2 ** 22 + 5
+    table, kv, new = to(np.zeros((n, width))), to([0] * n), to([2 ** 30] * n)
+    free = torch.arange(listed, dtype=torch.int32, device=dev())
+    count, offsets, status = to([listed]), to([7] * (n + 1)), to([9])
+    ws = torch.empty(dws.bevpool_assign_pages_workspace_size(n), dtype=torch.uint8, device=dev())
+    before = free.clone()
+    for lengths, want in (([2 ** 30] * 3, -1), ([2 ** 30, 2 ** 30, 0], -1), ([2 ** 30, 2 ** 30 - 1, 0], 0)):
+        new.copy_(to(lengths))
+        rc = tokens._lib().bevpool_assign_pages(
+            new.data_ptr(), None, kv.data_ptr(), kv.data_ptr(), n, table.data_ptr(), width, 1000, page,
+            free.data_ptr(), listed, count.data_ptr(), count.data_ptr(), offsets.data_ptr(), None, None,
+            2 ** 31 - 1, status.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert rc == 0 and int(status) == want
+        assert torch.equal(free, before)
+        if want:
+            assert not offsets.any() and not kv.any() and not table.any() and int(count) == listed
+    assert kv.tolist() == lengths and offsets.tolist() == [0, 2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1]
+    assert int(count) == listed - 2 ** 23
+    assert torch.equal(table[:2].reshape(-1), before.flip(0)[:2 ** 23])
 
 
 def test_wide_table_tokens():

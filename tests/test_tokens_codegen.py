@@ -91,3 +91,13 @@ def test_no_packed_fp32(codegen, name):
 @pytest.mark.parametrize("name", ["rope", "attention"])
 def test_saves_have_all_lanes(codegen, name):
     assert saved_before_restore(codegen[name][0]) == []
+
+
+def test_attention_scratch(codegen):
+    """16-bit caches take no scratch memory, e4m3 ones 24 bytes a lane at most (heads
+    over 96)."""
+    _, usage = codegen["attention"]
+    for k, u in usage.items():
+        m = re.search(r"attendILi\dELi(\d)ELi(\d+)E", k)
+        most = 24 if m and m.group(1) == "2" and int(m.group(2)) > 96 else 0
+        assert u["ScratchSize"] <= most, f"{k}: {u}"

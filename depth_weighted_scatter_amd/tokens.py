@@ -215,7 +215,8 @@ class PageTable:
     block_table [n_seqs, max_pages], kv_lengths [n_seqs] (cached tokens), and
     the pool's free pages: a stack free_pages [capacity] with free_count [1] of
     them, for pages of page_size tokens in a pool of n_pages (None: the
-    capacity).  q_offsets [n_seqs + 1] is made here where it is not given.
+    capacity).  q_offsets [n_seqs + 1] is made here, on the current stream, where
+    it is not given.
     Lengths and count are updated in place, or, where next_lengths and
     next_free are given, into those (a step that is planned while the last one
     still reads its lengths).  `batch` is the PagedBatch of the step that was
